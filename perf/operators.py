@@ -345,10 +345,10 @@ def run(s):
 
 
 def _caches(tsd, s):
-    """The program's cache descriptors, one per layer, made once."""
+    """The program's cache descriptors, made once."""
     if "caches" not in s:
         layers = [(s["k"], s["v"])] if s["k"].dim() == 4 else list(zip(s["k"], s["v"]))
-        s["caches"] = [tsd.KVCache(k, v, s["lens"], s["max_len"], page_table=s["table"]) for k, v in layers]
+        s["caches"] = tsd.LayerCaches(tsd.KVCache(k, v, s["lens"], s["max_len"], page_table=s["table"]) for k, v in layers)
     return s["caches"]
 
 
@@ -368,7 +368,7 @@ def _run_rope(s):
         if "rope" not in s:
             kw = {} if c["scaling"] == "none" else dict(scaling=c["scaling"], **SCALE)
             s["rope"] = tsd.RotaryEmbedding(rotary_dim=c["rotary_dim"], theta=c["theta"], interleaved=c["interleaved"], **kw)
-        cache = _caches(tsd, s)[0]
+        cache = _caches(tsd, s).caches[0]
         mask = depth = None
         if c["tree"]:
             mask, depth = tsd.tree_mask(s["parents"], s["indptr"], s["max_n"])
@@ -422,7 +422,7 @@ def _run_tree(s):
         import top_sparse_decode_topk_b200 as tsd
         if "queries" not in s:
             s["queries"] = tsd.Queries(s["q"], q_indptr=s["indptr"], max_tokens_per_seq=s["max_n"])
-        return list(tsd.tree_decode(_caches(tsd, s)[0], s["queries"], None if c["mask"] == "chain" else s["mask"],
+        return list(tsd.tree_decode(_caches(tsd, s).caches[0], s["queries"], None if c["mask"] == "chain" else s["mask"],
                                     out_dtype=DTYPES[c["out"]]))
     page, hkv, hq = c["page"], c["hkv"], c["hq"]
     B, N, L, G = s["lens"].numel(), s["max_n"], s["max_len"], hq // hkv
@@ -482,7 +482,7 @@ def _run_branch(s):
     if own:
         import top_sparse_decode_topk_b200 as tsd
         caches = _caches(tsd, s)
-        tsd.cache_fork(caches[0], s["refs"], s["src"], s["dst"])
+        tsd.cache_fork(caches, s["refs"], s["src"], s["dst"])
         tsd.cache_resize(caches, s["refs"], s["new_lens"])
     else:
         src, dst, page = s["src"].long(), s["dst"].long(), s["case"]["page"]
