@@ -27,7 +27,8 @@
  *    OR-ed into the status word at the start of the workspace; read it with
  *    tsd_read_device_status.
  *  - Workspace: each call takes (ws, ws_bytes) of at least the size returned by
- *    the matching *_workspace_size function.  Its first part must be zero when a
+ *    the matching *_workspace_size function (the calls of the last section have rules of
+ *    their own, stated there).  Its first part must be zero when a
  *    call starts; every call leaves it zero again, so zero it once (cudaMemset or
  *    tsd_workspace_init) after allocating it and again whenever the cache or
  *    query shape changes.  Calls that share a workspace must not overlap in time.
@@ -63,8 +64,13 @@ enum {
   TSD_DEV_BAD_PAGE = 1u << 2,  /* a page-table entry was outside [0, num_pages); row skipped */
   TSD_DEV_BAD_SEQ = 1u << 3,   /* seq_len outside [0, max_seq_len] or a bad q_indptr; the
                                   outputs of the affected sequence are not written          */
-  TSD_DEV_TIMEOUT = 1u << 4    /* a bounded wait inside a kernel gave up (an asynchronous
+  TSD_DEV_TIMEOUT = 1u << 4,   /* a bounded wait inside a kernel gave up (an asynchronous
                                   copy never completed); the results are not valid          */
+  TSD_DEV_BAD_TREE = 1u << 5,  /* a draft's parent was neither -1 nor an earlier draft; the
+                                  draft is taken as a child of the committed context        */
+  TSD_DEV_NO_PAGES = 1u << 6,  /* the free pages ran out; the sequence was left as it was   */
+  TSD_DEV_SHARED_PAGE = 1u << 7 /* a row to be moved lies in a page that several sequences
+                                  hold; the sequence was left as it was                     */
 };
 
 typedef enum {
@@ -416,6 +422,202 @@ tsd_status tsd_topk_select_label(const tsd_kv_cache* cache, const void* label_k,
                                  int32_t r, const tsd_queries* queries, int32_t k_max, const int32_t* k_per_token,
                                  int32_t* out_idx, int32_t* out_count, void* ws, size_t ws_bytes,
                                  tsd_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Speculative decoding over the paged cache.
+ *
+ * The pages ("Inference Time Context Sparsity: Illusion or Opportunity?") evaluate decode steps
+ * over a cache that is already filled and have no counterpart to these entry points.  They are
+ * what a serving loop does around such a step: take pages for the drafted tokens of every
+ * sequence (tsd_cache_resize), find each draft's ancestors (tsd_tree_mask), per layer write the
+ * drafts' rotated K and V rows (tsd_rope_append) and attend with the drafts as a tree
+ * (tsd_tree_decode), keep the accepted drafts (tsd_cache_compact) and give the surplus pages back
+ * (tsd_cache_resize).  tsd_cache_fork starts sequences that share another one's pages.
+ *
+ * As everywhere in this header, seq_lens[b] counts the n_b new tokens of the step, which are the
+ * last n_b tokens of the sequence: new token j sits at cache position seq_lens[b] - n_b + j.
+ * Shape arguments work as in tsd_queries (q_indptr NULL: one new token per sequence).  A sequence
+ * whose descriptor is bad (TSD_DEV_BAD_SEQ; here that includes n_b > seq_lens[b]) is skipped: its
+ * outputs are not written.
+ *
+ * status: device uint32 into which TSD_DEV_* bits are OR-ed, or NULL to drop them; the caller
+ * clears it (tsd_read_device_status reads and clears it).  These calls keep nothing in their
+ * workspace between calls, so it needs no initialisation; two calls that may overlap in time
+ * need a workspace each.  Unless stated otherwise, calls may run concurrently when they write
+ * different sequences' data.
+ * --------------------------------------------------------------------------------------- */
+
+/* A rotary embedding: pair i < rotary_dim/2 turns by turn[i] per position, in units of 2^-64 of
+ * a full turn, and cosines and sines are multiplied by mscale.  Filled by tsd_rope_init. */
+typedef struct {
+  int32_t rotary_dim;   /* even, 2 .. 128: dims [0, rotary_dim) are rotated, the rest copied */
+  int32_t interleaved;  /* nonzero: pairs (2i, 2i + 1); zero: pairs (i, i + rotary_dim / 2) */
+  float mscale;
+  uint32_t reserved;
+  uint64_t turn[64];
+} tsd_rope;
+
+typedef enum {
+  TSD_ROPE_PLAIN = 0,   /* f_i = theta^(-2i / rotary_dim) per position */
+  TSD_ROPE_LINEAR = 1,  /* f_i / factor */
+  TSD_ROPE_NTK = 2,     /* theta replaced by theta * factor^(rotary_dim / (rotary_dim - 2))
+                           (rotary_dim 2 has the one frequency 1, which theta does not change) */
+  TSD_ROPE_BANDED = 3,  /* with r = original_max_len f_i / (2 pi) turns over the trained length:
+                           f_i / factor for r <= low_freq_factor, f_i for r >= high_freq_factor,
+                           linear in r between */
+  TSD_ROPE_YARN = 4     /* YaRN (Peng et al., "YaRN: Efficient Context Window Extension of Large
+                           Language Models", 2023, section 3): f_i up to the dim that makes
+                           beta_fast turns over original_max_len (rounded down), f_i / factor from
+                           the dim that makes beta_slow turns (rounded up), linear in i between;
+                           mscale = attention_factor, by default 0.1 ln(factor) + 1 */
+} tsd_rope_scaling_kind;
+
+typedef struct {
+  int32_t kind;             /* tsd_rope_scaling_kind */
+  double factor;            /* >= 1 */
+  double original_max_len;  /* banded, yarn: > 0 */
+  double low_freq_factor;   /* banded: > 0 */
+  double high_freq_factor;  /* banded: > low_freq_factor */
+  double beta_fast;         /* yarn: > beta_slow */
+  double beta_slow;         /* yarn: > 0 */
+  double attention_factor;  /* yarn: 0 for the default */
+} tsd_rope_scaling;
+
+/* Host: fill `rope`.  scaling NULL means TSD_ROPE_PLAIN.  theta > 1.  Errors: INVALID_ARGUMENT,
+ * UNSUPPORTED (rotary_dim odd or outside [2, 128]). */
+tsd_status tsd_rope_init(tsd_rope* rope, int32_t rotary_dim, double theta, int32_t interleaved,
+                         const tsd_rope_scaling* scaling);
+
+/*
+ * Rotary positions of a step's queries and keys, and the step's K and V rows written into the
+ * cache.  For new token t = (b, j), cache position r = seq_lens[b] - n_b + j and angle
+ * position p = positions[t] if given, else seq_lens[b] - n_b + depth[t] if given, else r:
+ *   out_q[t, h]        = R(p) q[t, h]          in q's type
+ *   K[row of r, g]     = bf16(R(p) k_new[t, g])
+ *   V[row of r, g]     = bf16(v_new[t, g])
+ * R(p) turns pair i by p * turn[i]; angles are reduced exactly in 64-bit integers, so they keep
+ * fp32 accuracy at any position.  The arithmetic is fp32, rounded once.
+ * cache: k and v are written (pages named by the page table; a row whose page id is out of range
+ *   is skipped, TSD_DEV_BAD_PAGE).  A page that several sequences hold has to be made private
+ *   first (tsd_cache_resize does).
+ * queries: q (read with row stride q_stride), q_dtype, num_q_heads, num_tokens, q_indptr,
+ *   max_tokens_per_seq; causal and sm_scale are not used (sm_scale must still be positive).
+ * k_new, v_new: device, q's type, [T][Hkv][128].
+ * q_stride, k_stride, v_stride: elements from token to token (heads 128 apart), each a multiple
+ *   of 16 bytes and at least heads x 128; slices of one fused projection work.
+ * positions, depth: device int32 [T] or NULL, not both.
+ * out_q: device, q's type, [T][Hq][128] contiguous; may be q itself when q is contiguous.
+ * All rows 16-byte aligned.  Errors: INVALID_ARGUMENT, UNSUPPORTED, CUDA.
+ */
+tsd_status tsd_rope_append(const tsd_kv_cache* cache, const tsd_queries* queries, const tsd_rope* rope,
+                           int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+                           int64_t v_stride, const int32_t* positions, const int32_t* depth, void* out_q,
+                           uint32_t* status, tsd_stream_t stream);
+
+/*
+ * Trees of drafted tokens.  Sequence b's drafts are tokens q_indptr[b] .. q_indptr[b+1]-1 (q_indptr
+ * NULL: one per sequence); parents[t] is the index among the sequence's drafts of t's parent, an
+ * earlier draft, or -1 for a child of the committed context.
+ * mask : device uint32 [T][W], W = ceil(max_tokens / 32): bit i % 32 of word i / 32 of row t is set
+ *   when draft i is t itself or one of its ancestors.
+ * depth: device int32 [T] or NULL: number of t's ancestors among the drafts.
+ * max_tokens: host bound on the drafts of a sequence, at most 512.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (max_tokens > 512), CUDA.
+ */
+tsd_status tsd_tree_mask(int32_t batch, const int32_t* q_indptr, int32_t num_tokens, int32_t max_tokens,
+                         const int32_t* parents, uint32_t* mask, int32_t* depth, uint32_t* status,
+                         tsd_stream_t stream);
+
+/* Host: bytes of workspace tsd_tree_decode needs for these shapes on the current device (0 on
+ * invalid input).  As for sparse decode, it depends on the device's SM count. */
+size_t tsd_tree_decode_workspace_size(const tsd_kv_cache* cache, const tsd_queries* queries);
+
+/*
+ * Decode attention of drafted tokens that form a tree.  Draft j of sequence b sees the
+ * seq_lens[b] - n_b tokens before the drafts and those of the sequence's drafts whose bit is set
+ * in row t of `mask` (tsd_tree_mask writes such rows; any bits are allowed, so a draft need not
+ * see itself, and bits at or past n_b are ignored).  With S(t) those tokens and
+ * z_i = sm_scale q[t,h] . K[b,g,i]:
+ *   out[t,h] = sum over S(t) of exp(z_i - M) V[b,g,i] / sum over S(t) of exp(z_i - M)
+ *   lse[t,h] = M + ln sum over S(t) of exp(z_i - M),   M = max over S(t) of z_i
+ * and out = 0, lse = -inf where S(t) is empty.  Rows of V that a draft does not see do not reach
+ * its output, whatever they hold.
+ * mask: device uint32 [T][W], W = ceil(max_tokens_per_seq / 32), or NULL: draft j sees the drafts
+ *   up to itself, as tsd_dense_decode with causal set.  queries->causal must be nonzero.
+ * out, out_dtype, lse: as tsd_dense_decode.  max_tokens_per_seq <= 512.
+ * ws: at least tsd_tree_decode_workspace_size bytes, 256-byte aligned, not initialised.
+ * Errors: as tsd_dense_decode; UNSUPPORTED for max_tokens_per_seq > 512.
+ */
+tsd_status tsd_tree_decode(const tsd_kv_cache* cache, const tsd_queries* queries, const uint32_t* mask, void* out,
+                           int32_t out_dtype, float* lse, void* ws, size_t ws_bytes, uint32_t* status,
+                           tsd_stream_t stream);
+
+/* The K and V arrays of one layer; the layers of a model share a page table and lengths. */
+typedef struct {
+  void* k;
+  void* v;
+} tsd_layer;
+
+/*
+ * Sequences that start as copies of others: for each pair i < num_pairs, sequence dst[i], which
+ * must be empty (length 0), gets src[i]'s page-table row (-1 behind its last page) and length, and
+ * every page of the row is held once more (refs[page] += 1).  No K or V row is copied: a shared
+ * last page is copied by tsd_cache_resize when one of its holders grows.
+ * cache: paged; its page_table and seq_lens are WRITTEN.  refs: device int32 [num_pages], how many
+ *   table entries hold each page; 0 marks a free page.
+ * A pair is skipped, with TSD_DEV_BAD_SEQ, when an index is out of range, src[i] == dst[i], dst[i]
+ * is not empty, an earlier pair has the same dst, or src[i] is some pair's dst.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (contiguous layout), CUDA.
+ */
+tsd_status tsd_cache_fork(const tsd_kv_cache* cache, int32_t* refs, int32_t num_pairs, const int32_t* src,
+                          const int32_t* dst, uint32_t* status, tsd_stream_t stream);
+
+/* Host: bytes of workspace tsd_cache_resize needs (0 on invalid input). */
+size_t tsd_cache_resize_workspace_size(const tsd_kv_cache* cache);
+
+/*
+ * Take and release pages: sequence b goes from seq_lens[b] to new_lens[b] tokens.
+ *  - Growing, it takes pages for the tokens its pages have no room for.  When its last page is
+ *    partly filled and held by others too (refs > 1 when the call starts), that page is replaced
+ *    by a copy of its own -- in every layer -- and held once less; every sequence growing out of a
+ *    shared page gets a copy, and a page nobody holds any more is free.
+ *  - Shrinking, it releases the pages behind its new last one (refs -= 1, table entry -1).
+ *    new_lens[b] = 0 ends a sequence.
+ * Pages are taken from those that are free (refs == 0) when the call starts, the lowest numbers
+ * first, in order of sequence and position (the replaced last page first).  When the pages wanted
+ * by sequences 0 .. b exceed the free ones, a sequence b that wants any is left as it was
+ * (TSD_DEV_NO_PAGES).  A new_lens[b] outside [0, max_seq_len] leaves it so too (TSD_DEV_BAD_SEQ).  A
+ * table entry out of range is not released (TSD_DEV_BAD_PAGE), nor is a page that refs has as free.
+ * cache: paged; its page_table and seq_lens are WRITTEN.  refs: as tsd_cache_fork, written.
+ * layers: host array of num_layers (1 .. 128) layers' K and V, each laid out like cache->k; pages
+ *   are copied in all of them (cache->k and v only if they are among them).
+ * ws: at least tsd_cache_resize_workspace_size bytes, 256-byte aligned, not initialised.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (contiguous layout, more than 128 layers),
+ * WORKSPACE_TOO_SMALL, CUDA.
+ */
+tsd_status tsd_cache_resize(const tsd_kv_cache* cache, int32_t num_layers, const tsd_layer* layers, int32_t* refs,
+                            const int32_t* new_lens, void* ws, size_t ws_bytes, uint32_t* status,
+                            tsd_stream_t stream);
+
+/*
+ * Keep the accepted drafts: in every layer, row seq_lens[b] - n_b + keep[b][i] of sequence b moves
+ * to row seq_lens[b] - n_b + i, for the leading entries of keep[b] that are >= 0, and
+ * out_lens[b] = seq_lens[b] - n_b + their number.  Lengths and pages stay as they are: pass
+ * out_lens to tsd_cache_resize.
+ * n_b is given by q_indptr, num_tokens and max_tokens as in tsd_tree_mask.
+ * keep: device int32 [batch][k_max], strictly ascending draft indices below n_b, then -1.  A list
+ *   that is not leaves its sequence as it was, with out_lens[b] = seq_lens[b] (TSD_DEV_BAD_INDEX); so
+ *   do a bad page among the rows named (TSD_DEV_BAD_PAGE), a bad descriptor (TSD_DEV_BAD_SEQ) and,
+ *   when refs (device int32 [num_pages], may be NULL) is given, a row to be written that lies in a page
+ *   with refs > 1 (TSD_DEV_SHARED_PAGE).
+ * out_lens: device int32 [batch], not overlapping seq_lens.
+ * layers, num_layers: as tsd_cache_resize (contiguous layouts work too).
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED, CUDA.
+ */
+tsd_status tsd_cache_compact(const tsd_kv_cache* cache, int32_t num_layers, const tsd_layer* layers,
+                             const int32_t* q_indptr, int32_t num_tokens, int32_t max_tokens, const int32_t* keep,
+                             int32_t k_max, const int32_t* refs, int32_t* out_lens, uint32_t* status,
+                             tsd_stream_t stream);
 
 #ifdef __cplusplus
 }

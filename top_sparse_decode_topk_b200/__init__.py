@@ -14,6 +14,10 @@ Opportunity?" (gist.science technical summary, section 2 "Oracle Top-K" and
     out, lse   = sparse_decode(cache, queries, idx)      # attention over the kept rows
     out, lse   = dense_decode(cache, queries)            # attention over every row
 
+What a serving loop does around such a step on the paged cache -- rotary positions and the append
+of new rows, attention for trees of drafted tokens, pages taken, shared, compacted and released -- is
+in ``speculative`` and available here under the same names.
+
 There is no fallback: if ``libtsd.so`` is missing or a call fails, an
 exception is raised.
 """
@@ -30,7 +34,9 @@ __all__ = [
     "KVCache", "Queries", "Workspace", "TsdError", "topk_select", "sparse_decode", "dense_decode",
     "LabelIndex", "label_channels", "label_cache_build", "topk_select_label", "stochastic_select",
     "read_device_status", "library_path", "load_library", "DEV_BAD_INDEX", "DEV_UNSORTED",
-    "DEV_BAD_PAGE", "DEV_BAD_SEQ",
+    "DEV_BAD_PAGE", "DEV_BAD_SEQ", "DEV_TIMEOUT", "DEV_BAD_TREE", "DEV_NO_PAGES", "DEV_SHARED_PAGE",
+    "RotaryEmbedding", "rope_append", "tree_mask", "tree_decode", "LayerCaches", "cache_fork", "cache_resize",
+    "cache_compact",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -40,6 +46,7 @@ TSD_ERR_WORKSPACE_TOO_SMALL, TSD_ERR_CUDA, TSD_ERR_DEVICE_STATUS = 3, 4, 5
 TSD_BF16, TSD_F32 = 0, 1
 LAYOUT_PAGED, LAYOUT_CONTIGUOUS = 0, 1
 DEV_BAD_INDEX, DEV_UNSORTED, DEV_BAD_PAGE, DEV_BAD_SEQ = 1, 2, 4, 8
+DEV_TIMEOUT, DEV_BAD_TREE, DEV_NO_PAGES, DEV_SHARED_PAGE = 16, 32, 64, 128
 
 
 class TsdError(RuntimeError):
@@ -64,6 +71,23 @@ class _QueriesC(ctypes.Structure):
         ("num_tokens", ctypes.c_int32), ("q_indptr", ctypes.c_void_p),
         ("max_tokens_per_seq", ctypes.c_int32), ("causal", ctypes.c_int32), ("sm_scale", ctypes.c_float),
     ]
+
+
+class _RopeC(ctypes.Structure):
+    _fields_ = [
+        ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("mscale", ctypes.c_float),
+        ("reserved", ctypes.c_uint32), ("turn", ctypes.c_uint64 * 64),
+    ]
+
+
+class _RopeScalingC(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32)] + [(name, ctypes.c_double) for name in (
+        "factor", "original_max_len", "low_freq_factor", "high_freq_factor", "beta_fast", "beta_slow",
+        "attention_factor")]
+
+
+class _LayerC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
 
 
 EXPORTS = {
@@ -128,6 +152,29 @@ EXPORTS = {
                                              ctypes.c_int32, ctypes.POINTER(_QueriesC), ctypes.c_int32,
                                              ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                              ctypes.c_size_t, ctypes.c_void_p]),
+    "tsd_rope_init": (ctypes.c_int, [ctypes.POINTER(_RopeC), ctypes.c_int32, ctypes.c_double, ctypes.c_int32,
+                                     ctypes.POINTER(_RopeScalingC)]),
+    "tsd_rope_append": (ctypes.c_int, [ctypes.POINTER(_KvCacheC), ctypes.POINTER(_QueriesC), ctypes.POINTER(_RopeC),
+                                       ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                       ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_void_p]),
+    "tsd_tree_mask": (ctypes.c_int, [ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_void_p]),
+    "tsd_tree_decode_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(_KvCacheC), ctypes.POINTER(_QueriesC)]),
+    "tsd_tree_decode": (ctypes.c_int, [ctypes.POINTER(_KvCacheC), ctypes.POINTER(_QueriesC), ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
+    "tsd_cache_fork": (ctypes.c_int, [ctypes.POINTER(_KvCacheC), ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "tsd_cache_resize_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(_KvCacheC)]),
+    "tsd_cache_resize": (ctypes.c_int, [ctypes.POINTER(_KvCacheC), ctypes.c_int32, ctypes.POINTER(_LayerC),
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                        ctypes.c_void_p, ctypes.c_void_p]),
+    "tsd_cache_compact": (ctypes.c_int, [ctypes.POINTER(_KvCacheC), ctypes.c_int32, ctypes.POINTER(_LayerC),
+                                         ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                         ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_void_p]),
 }
 
 _LIB = None
@@ -669,17 +716,33 @@ def dense_decode(cache: KVCache, queries: Queries, out=None, out_dtype=None, lse
     return _finish(out, host_out, lse, host_lse, s)
 
 
-def read_device_status(workspace: Optional[Workspace] = None, device=None, stream=None) -> int:
-    """Read and clear the device status bits of a workspace (synchronises the stream)."""
-    import torch
-    lib = load_library()
-    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-    ws = _ws(workspace, dev)
-    if ws.buf is None:
-        return 0
-    s, sp = _stream_ptr(stream, ws.buf.device)
+def _read_status(ptr, device, stream) -> int:
+    s, sp = _stream_ptr(stream, device)
     flags = ctypes.c_uint32(0)
-    rc = lib.tsd_read_device_status(ws.buf.data_ptr(), sp, ctypes.byref(flags))
+    rc = load_library().tsd_read_device_status(ptr, sp, ctypes.byref(flags))
     if rc not in (TSD_OK, TSD_ERR_DEVICE_STATUS):
         raise TsdError(rc, "tsd_read_device_status")
     return int(flags.value)
+
+
+def read_device_status(workspace: Optional[Workspace] = None, device=None, stream=None) -> int:
+    """Read and clear the device status bits of a workspace (synchronises the stream).  Without a
+    workspace: those of the device's default workspace and of the calls that were given neither a
+    workspace nor a status word."""
+    import torch
+    load_library()
+    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    ws = _ws(workspace, dev)
+    flags = 0
+    if ws.buf is not None:
+        flags |= _read_status(ws.buf.data_ptr(), ws.buf.device, stream)
+    if workspace is None:
+        word = speculative._STATUS.get(dev.index if dev.index is not None else torch.cuda.current_device())
+        if word is not None:
+            flags |= _read_status(word.data_ptr(), word.device, stream)
+    return flags
+
+
+from . import speculative   # noqa: E402  (needs the declarations above)
+from .speculative import (LayerCaches, RotaryEmbedding, cache_compact, cache_fork, cache_resize,   # noqa: E402
+                          rope_append, tree_decode, tree_mask)

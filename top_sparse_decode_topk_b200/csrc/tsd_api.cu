@@ -16,6 +16,7 @@
 #include "tsd_filter.cuh"
 
 #include "tsd_args.h"
+#include "tsd_host.h"
 #include "tsd_kvtile.cuh"
 
 namespace tsd {
@@ -43,7 +44,7 @@ cudaError_t launch_label_topk(const TopkArgs& a, const uint16_t* label, const in
 
 using namespace tsd;
 
-namespace {
+namespace tsd {
 
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 
@@ -119,22 +120,17 @@ tsd_status check_inputs(const tsd_kv_cache* c, const tsd_queries* q, KvView* kv,
   return TSD_OK;
 }
 
-tsd_status cuda_status(cudaError_t e) { return e == cudaSuccess ? TSD_OK : TSD_ERR_CUDA; }
-
-// Tensor maps of the K and V caches seen as [rows][128] bf16 with a {64, box_rows} box and
-// 128-byte swizzling, for the TMA loads of the dense-tile kernels.  Caches whose pages
-// are smaller than 8 tokens do not use them (their tiles are copied with cp.async).
-tsd_status make_kv_maps(const tsd_kv_cache* c, KvMaps* maps) {
+tsd_status make_kv_maps(const tsd_kv_cache* c, KvMaps* maps, int max_box) {
   memset(maps, 0, sizeof(*maps));
   int64_t rows;
   int box_rows;
   if (c->layout == TSD_LAYOUT_CONTIGUOUS) {
     rows = (int64_t)c->batch * c->num_kv_heads * c->max_seq_len;
-    box_rows = 16;
+    box_rows = max_box;
   } else {
     if (c->page_size < 8) return TSD_OK;
     rows = c->num_pages * c->num_kv_heads * c->page_size;
-    box_rows = c->page_size < 16 ? c->page_size : 16;
+    box_rows = c->page_size < max_box ? c->page_size : max_box;
   }
   if (rows >= (int64_t)1 << 31) return TSD_ERR_UNSUPPORTED;
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
@@ -165,7 +161,58 @@ tsd_status make_kv_maps(const tsd_kv_cache* c, KvMaps* maps) {
   return TSD_OK;
 }
 
-}  // namespace
+// SM count of the current device: the sparse plan sizes its grid to the resident CTAs.  A
+// B200's 148 when no device can be queried (host-only sizing calls on a machine without one).
+int current_sm_count() {
+  constexpr int kMaxDev = 64;
+  static std::mutex mu;
+  static int cache[kMaxDev] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) {
+    cudaGetLastError();
+    return 148;
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  if (cache[dev] == 0) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = 148;
+    }
+    cache[dev] = n;
+  }
+  return cache[dev];
+}
+
+tsd_status sizes_for(const tsd_kv_cache* cache, const tsd_queries* queries, Shapes* sh) {
+  if (cache == nullptr || queries == nullptr) return TSD_ERR_INVALID_ARGUMENT;
+  KvView kv; QView qv;
+  tsd_kv_cache c = *cache;
+  tsd_queries q = *queries;
+  static const uint16_t dummy[8] = {0};
+  if (c.k == nullptr) c.k = dummy;
+  if (c.v == nullptr) c.v = dummy;
+  if (c.seq_lens == nullptr) c.seq_lens = reinterpret_cast<const int32_t*>(dummy);
+  if (c.layout == TSD_LAYOUT_PAGED && c.page_table == nullptr) c.page_table = reinterpret_cast<const int32_t*>(dummy);
+  if (q.q == nullptr) q.q = dummy;
+  return check_inputs(&c, &q, &kv, &qv, sh);
+}
+
+// The cache descriptor alone, validated through check_inputs with a stand-in query set.
+tsd_status check_cache_only(const tsd_kv_cache* cache, KvView* kv, Shapes* sh) {
+  if (cache == nullptr) return TSD_ERR_INVALID_ARGUMENT;
+  tsd_queries q;
+  memset(&q, 0, sizeof(q));
+  q.q = cache->k;
+  q.q_dtype = TSD_BF16;
+  q.num_q_heads = cache->num_kv_heads;
+  q.num_tokens = cache->batch;
+  q.sm_scale = 1.f;
+  QView qv;
+  return check_inputs(cache, &q, kv, &qv, sh);
+}
+
+}  // namespace tsd
 
 extern "C" {
 
@@ -217,29 +264,6 @@ size_t tsd_topk_workspace_size(const tsd_kv_cache* cache, const tsd_queries* que
   return topk_layout_for(sh, topk_filter_space(sh, k_max)).total;
 }
 
-// SM count of the current device: the sparse plan sizes its grid to the resident CTAs.  A
-// B200's 148 when no device can be queried (host-only sizing calls on a machine without one).
-static int current_sm_count() {
-  constexpr int kMaxDev = 64;
-  static std::mutex mu;
-  static int cache[kMaxDev] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) {
-    cudaGetLastError();
-    return 148;
-  }
-  std::lock_guard<std::mutex> lock(mu);
-  if (cache[dev] == 0) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-      cudaGetLastError();
-      n = 148;
-    }
-    cache[dev] = n;
-  }
-  return cache[dev];
-}
-
 // Work decomposition of tsd_sparse_decode.  The one-task-per-warp kernel fits its grid to one
 // wave of resident CTAs.  The persistent kernel takes the call instead when that plan needs
 // more than one wave, or when it fits one wave only by giving every warp a whole list of 256
@@ -264,20 +288,6 @@ static SparsePlan sparse_plan(const Shapes& sh, int k_max) {
     stream = ctas > (int64_t)sms * kSpCtasPerSm || (wave.nsplit == 1 && k_max >= 256);
   }
   return stream ? plan_sparse_stream(sh, k_max, sms, e_override) : wave;
-}
-
-static tsd_status sizes_for(const tsd_kv_cache* cache, const tsd_queries* queries, Shapes* sh) {
-  if (cache == nullptr || queries == nullptr) return TSD_ERR_INVALID_ARGUMENT;
-  KvView kv; QView qv;
-  tsd_kv_cache c = *cache;
-  tsd_queries q = *queries;
-  static const uint16_t dummy[8] = {0};
-  if (c.k == nullptr) c.k = dummy;
-  if (c.v == nullptr) c.v = dummy;
-  if (c.seq_lens == nullptr) c.seq_lens = reinterpret_cast<const int32_t*>(dummy);
-  if (c.layout == TSD_LAYOUT_PAGED && c.page_table == nullptr) c.page_table = reinterpret_cast<const int32_t*>(dummy);
-  if (q.q == nullptr) q.q = dummy;
-  return check_inputs(&c, &q, &kv, &qv, sh);
 }
 
 size_t tsd_sparse_decode_workspace_size(const tsd_kv_cache* cache, const tsd_queries* queries, int32_t k_max) {
@@ -690,20 +700,6 @@ tsd_status tsd_dense_decode(const tsd_kv_cache* cache, const tsd_queries* querie
 // Label-channel approximate indexer
 // ---------------------------------------------------------------------------
 static bool label_r_ok(int32_t r) { return r == 8 || r == 16 || r == 32; }
-
-// The cache descriptor alone, validated through check_inputs with a stand-in query set.
-static tsd_status check_cache_only(const tsd_kv_cache* cache, KvView* kv, Shapes* sh) {
-  if (cache == nullptr) return TSD_ERR_INVALID_ARGUMENT;
-  tsd_queries q;
-  memset(&q, 0, sizeof(q));
-  q.q = cache->k;
-  q.q_dtype = TSD_BF16;
-  q.num_q_heads = cache->num_kv_heads;
-  q.num_tokens = cache->batch;
-  q.sm_scale = 1.f;
-  QView qv;
-  return check_inputs(cache, &q, kv, &qv, sh);
-}
 
 static int64_t cache_rows(const tsd_kv_cache* c) {
   return c->layout == TSD_LAYOUT_CONTIGUOUS ? (int64_t)c->batch * c->num_kv_heads * c->max_seq_len

@@ -66,6 +66,11 @@ __device__ __forceinline__ void flag_status(uint32_t* status, uint32_t bits) {
   atomicOr(status, bits);
 }
 
+// The same for entry points whose status pointer may be NULL.
+__device__ __forceinline__ void flag_optional(uint32_t* status, uint32_t bits) {
+  if (status != nullptr) atomicOr(status, bits);
+}
+
 // The raw descriptor of sequence b (seq_lens[b] and its q_indptr range), loaded but not yet
 // checked, so that a kernel can put other loads in flight before it waits on these.
 struct SeqRaw {
@@ -162,6 +167,13 @@ __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
   uint32_t u = __float_as_uint(f);
   u += 0x7FFFu + ((u >> 16) & 1u);
   return (uint16_t)(u >> 16);
+}
+
+// Two fp32 -> packed bf16x2, round to nearest even, NaN kept; lo in the low half.
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 // Order-preserving map of an fp32 score onto uint32 (larger score -> larger key);
