@@ -120,7 +120,7 @@ tsd_status check_inputs(const tsd_kv_cache* c, const tsd_queries* q, KvView* kv,
   return TSD_OK;
 }
 
-tsd_status make_kv_maps(const tsd_kv_cache* c, KvMaps* maps, int max_box) {
+tsd_status make_kv_maps(const tsd_kv_cache* c, KvMaps* maps, int max_box, bool gather) {
   memset(maps, 0, sizeof(*maps));
   int64_t rows;
   int box_rows;
@@ -128,9 +128,9 @@ tsd_status make_kv_maps(const tsd_kv_cache* c, KvMaps* maps, int max_box) {
     rows = (int64_t)c->batch * c->num_kv_heads * c->max_seq_len;
     box_rows = max_box;
   } else {
-    if (c->page_size < 8) return TSD_OK;
+    if (c->page_size < 8 && !gather) return TSD_OK;
     rows = c->num_pages * c->num_kv_heads * c->page_size;
-    box_rows = c->page_size < max_box ? c->page_size : max_box;
+    box_rows = c->page_size < 8 ? 1 : (c->page_size < max_box ? c->page_size : max_box);
   }
   if (rows >= (int64_t)1 << 31) return TSD_ERR_UNSUPPORTED;
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;

@@ -286,6 +286,13 @@ __device__ __forceinline__ uint64_t l2_evict_first() {
   return p;
 }
 
+// The ordinary L2 policy, for loads whose policy is chosen at run time.
+__device__ __forceinline__ uint64_t l2_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;\n" : "=l"(p));
+  return p;
+}
+
 // 2-D tiled TMA load (box given by the tensor map) into shared memory under an L2 cache
 // policy, completion counted on `bar`.  x is the innermost (element) coordinate and must be a
 // multiple of 8 for bf16 (16 bytes); y is the row.
@@ -295,6 +302,17 @@ __device__ __forceinline__ void tma_load_2d_hint(void* dst, const void* tmap, in
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
       " [%0], [%1, {%2, %3}], [%4], %5;\n" ::"r"(smem_u32(dst)),
       "l"(tmap), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+// Four rows y[0..3] (each 64 bf16 from column x) of a tensor map whose box is one row high, to four
+// consecutive 128-byte rows of shared memory.
+__device__ __forceinline__ void tma_gather4_hint(void* dst, const void* tmap, int x, const int* y, uint64_t* bar,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;\n" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
 }
 
