@@ -528,9 +528,9 @@ tsd_status tsd_tree_mask(int32_t batch, const int32_t* q_indptr, int32_t num_tok
                          const int32_t* parents, uint32_t* mask, int32_t* depth, uint32_t* status,
                          tsd_stream_t stream);
 
-/* Host: bytes of workspace tsd_tree_decode needs for these shapes on the current device (0 on
- * invalid input).  As for sparse decode, it depends on the device's SM count. */
-size_t tsd_tree_decode_workspace_size(const tsd_kv_cache* cache, const tsd_queries* queries);
+/* Host: bytes of workspace tsd_tree_decode needs for these shapes and output type on the current
+ * device (0 on invalid input).  As for sparse decode, it depends on the device's SM count. */
+size_t tsd_tree_decode_workspace_size(const tsd_kv_cache* cache, const tsd_queries* queries, int32_t out_dtype);
 
 /*
  * Decode attention of drafted tokens that form a tree.  Draft j of sequence b sees the

@@ -112,8 +112,9 @@ def test_tree_decode_errors_before_launch(lib):
     q.causal = 0
     assert call(q=q) == INVALID
     assert lib.tsd_tree_decode(None, ctypes.byref(q), None, FAKE, 0, None, FAKE, 1 << 40, None, None) == INVALID
-    assert lib.tsd_tree_decode_workspace_size(ctypes.byref(make_cache(head_dim=64)), ctypes.byref(make_queries())) == 0
-    assert lib.tsd_tree_decode_workspace_size(ctypes.byref(make_cache()), ctypes.byref(make_queries())) > 0
+    assert lib.tsd_tree_decode_workspace_size(ctypes.byref(make_cache(head_dim=64)), ctypes.byref(make_queries()), 0) == 0
+    assert lib.tsd_tree_decode_workspace_size(ctypes.byref(make_cache()), ctypes.byref(make_queries()), 0) > 0
+    assert lib.tsd_tree_decode_workspace_size(ctypes.byref(make_cache()), ctypes.byref(make_queries()), 7) == 0
 
 
 def layers(n, k=FAKE, v=FAKE):

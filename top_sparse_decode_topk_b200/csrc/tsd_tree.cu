@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kTmThreads) tree_mask_kernel(TreeMaskArgs a) {
 // order of the shares.
 //
 // A CTA: warps 0-3 and 4-7 are two streams of 128 lists, one list a thread (= a tensor-memory lane);
-// warp 8 issues the MMAs; warp 9 loads K and V tiles by TMA.
+// warps 8 and 9 issue a stream's MMAs; warps 10 and 11 load the K and V tiles by TMA.
 //   S_s = Q_s K^T   (M 128, N TT, K 128; operands in shared memory, fp32 in tensor memory)
 //   softmax in registers: running maximum and sum per thread, P rounded to bf16 into tensor memory
 //   O_s += P_s V    (M 128, N 128, K TT; P from tensor memory, V MN-major from shared memory)
@@ -133,21 +133,32 @@ struct TreeArgs {
   int64_t* line;       // [0] tiles in all, [1 + b] first tile of sequence b
   float2* part_ml;     // [2 * CTAs][part_rows] (maximum, sum), base-2 units
   float4* part_acc;    // [2 * CTAs][32][part_rows] four dims of an unnormalised row
+  float4* sums;        // [CTAs][2][32][128] sums of a stream's products (fp32 outputs)
   int32_t ctas;
 };
 
-constexpr int kTaThreads = 320;
+constexpr int kTaThreads = 384;
 constexpr int kTaRowsPerStream = 128;
 constexpr int kTaTiles = 229376;               // Q tiles and the ring
 constexpr size_t kTaSmem = kTaTiles + 3072;    // then barriers and scratch: all of an SM's shared memory
 
 template <int QP, int PP>
 struct TreeShape {
-  static constexpr int TT = QP == 1 && PP == 1 ? 128 : 64;   // tokens of a tile
+  static constexpr int TT = PP == 1 ? 64 : 32;               // tokens of a tile
   static constexpr int kRows = QP == 1 ? 256 : 128;          // lists of a unit: two Q tiles, or one in three parts
   static constexpr int kQBytes = (QP == 1 ? 2 : 3) * 32768;
   static constexpr int kSlotBytes = TT * 256;                // one K or V tile
+  // Ring slots of K and of V.  A K tile is done with once its scores are made, a V tile waits for the
+  // softmax in between.
   static constexpr int kSlots = (kTaTiles - kQBytes) / kSlotBytes;
+  // Both even: where the streams take alternate tiles, a slot then serves one stream throughout a
+  // segment, and its waits see every phase of the slot's barriers (a parity says no more than that).
+  static constexpr int kKSlots = (kSlots * 2 / 5 + 1) & ~1, kVSlots = kSlots - kKSlots;
+  static_assert(kKSlots % 2 == 0 && kVSlots % 2 == 0 && kKSlots >= 4 && kVSlots >= 4, "ring slots");
+  // Steps whose products add up in tensor memory before they are moved to fp32 sums in global
+  // memory (fp32 outputs only; 0: never).  The tensor cores truncate each sum: measured, V = 1 came out
+  // 6.6e-9 low per accumulation, 2e-5 over 80000 tokens.
+  static constexpr int kFlush = PP == 1 ? 0 : 16;
 };
 
 // What one sequence contributes: its descriptor and its units.
@@ -219,12 +230,14 @@ struct TreeWalk {
 
 // Shared-memory control block behind the Q tiles and the ring.
 struct TreeCtl {
-  uint64_t full[16], empty[16];
-  uint64_t q_ready, s_full[2], p_ready[2], o_done[2], fixed[2], drain;
-  uint32_t abort, tmem, nf[2][4];
-  // Rows with a bad page of tile m (counted over the CTA's share), at m % 16: the producer is at
-  // most (kSlots + 1) / 2 tiles ahead of the softmax, whose tile's V it waits for.
-  uint32_t bad[16][4];
+  uint64_t k_full[8], k_empty[8], v_full[12], v_empty[12];
+  // [stream][buffer of S and P]: step k of a stream uses buffer k % 2 and these barriers' phase k / 2.
+  // s_full of step k implies that the products of step k - 2 are done, so no wait is two phases behind.
+  uint64_t q_ready, s_full[2][2], p_ready[2][2], o_done[2][2], fixed[2], drain[2];
+  uint32_t abort, tmem, nf[2][2];
+  // Rows with a bad page of tile m (counted over the CTA's share), at m % 32: K is loaded at most
+  // 4 (two steps of two streams) + kKSlots <= 12 tiles ahead of the softmax.
+  uint32_t bad[32][2];
   int64_t scan[10];
   int64_t total, off;
   int b0;
@@ -256,10 +269,15 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
   __syncwarp();
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u); }
 
 // The tokens [tw, tw + 32) that draft j of the sequence sees, as bits.
-__device__ __forceinline__ uint32_t tree_visible(const TreeArgs& a, const TreeSeq& s, int j, int tw) {
+__device__ __forceinline__ uint32_t tree_visible32(const TreeArgs& a, const TreeSeq& s, int j, int tw) {
   const int d0 = tw - s.base;   // draft index of the first token
   uint32_t bits = 0;
   if (d0 + 31 >= 0 && d0 < s.n) {
@@ -278,29 +296,149 @@ __device__ __forceinline__ uint32_t tree_visible(const TreeArgs& a, const TreeSe
   }
   return (low_bits(-d0) | bits) & low_bits(s.len - tw);
 }
-
-// K or V tile `tile` of a segment into shared memory by TMA, all 32 lanes of the producer issuing.
-// y: this lane's box coordinates, one box a lane (pages of 8 or more tokens: box rows `bp`), or four
-// rows a lane (smaller pages).
+// The same for a tile of TT tokens.
 template <int TT>
-__device__ __forceinline__ void tree_issue(const CUtensorMap* map, unsigned char* dst, uint64_t* bar, const int (&y)[4],
-                                           int bp, int rows, int lane, uint64_t pol) {
-  if (bp >= 8) {
-    const int boxes = (rows + bp - 1) / bp;
-    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * bp * 256));
+__device__ __noinline__ uint64_t tree_visible(const TreeArgs& a, TreeSeq s, int j, int tw) {
+  uint64_t v = tree_visible32(a, s, j, tw);
+  if (TT > 32) v |= (uint64_t)tree_visible32(a, s, j, tw + 32) << 32;
+  return v;
+}
+
+// The paths that few tiles take stand outside the softmax loop, so that they cost it no registers (168
+// a thread; what spills goes to L2, since shared memory takes nearly all of the L1).
+
+// O of this warp's lists times f.
+__device__ __noinline__ void tree_scale(uint32_t to, float f) {
+  for (int c = 0; c < 4; ++c) {
+    float o[32];
+    tmem_ld32(to + c * 32, o);
+    tmem_wait_ld();
+    tmem_loaded32(o);
+#pragma unroll
+    for (int d = 0; d < 32; ++d) o[d] *= f;
+    tmem_st32(to + c * 32, o);
+  }
+  tmem_wait_st();
+}
+
+// sums = sums * f + O (sums are taken as 0 when !have): this list's column of [32][128] float4.
+__device__ __noinline__ void tree_flush(uint32_t to, float4* sums, float f, bool have, bool valid) {
+  for (int c = 0; c < 4; ++c) {
+    float o[32];
     __syncwarp();
-    if (lane < boxes) {
-      tma_load_2d_hint(dst + lane * bp * 128, map, 0, y[0], bar, pol);
-      tma_load_2d_hint(dst + TT * 128 + lane * bp * 128, map, 64, y[0], bar, pol);
+    tmem_ld32(to + c * 32, o);
+    tmem_wait_ld();
+    tmem_loaded32(o);
+    if (!valid) continue;
+#pragma unroll
+    for (int d = 0; d < 8; ++d) {
+      float4* p = sums + (8 * c + d) * kTaRowsPerStream;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (have) x = __ldcg(p);
+      __stcg(p, make_float4(x.x * f + o[4 * d], x.y * f + o[4 * d + 1], x.z * f + o[4 * d + 2], x.w * f + o[4 * d + 3]));
     }
-  } else {
-    const int groups = (rows + 3) >> 2;
-    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(groups * 4 * 256));
+  }
+}
+
+// O += sums * f.
+__device__ __noinline__ void tree_unflush(uint32_t to, const float4* sums, float f, bool valid) {
+  for (int c = 0; c < 4; ++c) {
+    float o[32];
     __syncwarp();
-    if (lane < groups) {
-      tma_gather4_hint(dst + lane * 512, map, 0, y, bar, pol);
-      tma_gather4_hint(dst + TT * 128 + lane * 512, map, 64, y, bar, pol);
+    tmem_ld32(to + c * 32, o);
+    tmem_wait_ld();
+    tmem_loaded32(o);
+    if (valid) {
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        const float4 x = __ldcg(sums + (8 * c + d) * kTaRowsPerStream);
+        o[4 * d] += f * x.x;
+        o[4 * d + 1] += f * x.y;
+        o[4 * d + 2] += f * x.z;
+        o[4 * d + 3] += f * x.w;
+      }
     }
+    __syncwarp();
+    tmem_st32(to + c * 32, o);
+  }
+  tmem_wait_st();
+}
+
+// A special tile's V in shared memory (`threads` threads, index id, share the work; bar is theirs): rows
+// behind the sequence and drafts' rows that are not finite become zeros.  Returns the latter as bits.
+template <int TT>
+__device__ __noinline__ uint64_t tree_clean_v(unsigned char* vt, uint32_t* found, int t0, int base, int len, int id,
+                                              int threads, int bar) {
+  named_sync(bar, threads);
+  if (id < 2) found[id] = 0;
+  named_sync(bar, threads);
+  for (int e = id; e < TT * 16; e += threads) {
+    const int r = e >> 4, ch = e & 15, t = t0 + r;
+    if (t < base) continue;
+    uint4* p = reinterpret_cast<uint4*>(vt + (ch >> 3) * (TT * 128) + sw128(r, ch & 7));
+    if (t >= len) {
+      *p = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const uint4 v = *p;
+    uint32_t odd = 0;   // an exponent of all ones
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t u = w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
+      odd |= ((u & 0x7F80u) == 0x7F80u) | ((u & 0x7F800000u) == 0x7F800000u);
+    }
+    if (odd) atomicOr(&found[r >> 5], 1u << (r & 31));
+  }
+  named_sync(bar, threads);
+  const uint64_t any = (uint64_t)found[1] << 32 | found[0];
+  if (any) {
+    for (int e = id; e < TT * 16; e += threads) {
+      const int r = e >> 4, ch = e & 15;
+      if (any >> r & 1)
+        *reinterpret_cast<uint4*>(vt + (ch >> 3) * (TT * 128) + sw128(r, ch & 7)) = make_uint4(0, 0, 0, 0);
+    }
+  }
+  asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+  if (threads == 256) named_sync(bar, threads);   // the other stream's products read these rows too
+  return any;
+}
+
+// Adds to O the products of the rows of V that were zeroed for their infinities or NaNs (`rows`), for
+// the lists that see them (`seen`).  The tile's P is still in tensor memory, at tp.
+template <int TT, int PP>
+__device__ __noinline__ void tree_add_nonfinite(const KvView& kv, int b, int g, int t0, uint64_t rows, uint64_t seen,
+                                                uint32_t tp, uint32_t to) {
+  for (; rows != 0; rows &= rows - 1) {
+    const int r = __ffsll((long long)rows) - 1;
+    float p = 0.f;
+    for (int part = 0; part < PP; ++part) {
+      uint32_t w = tmem_ld1(tp + part * (TT / 2) + (r >> 1));
+      tmem_wait_ld();
+      asm volatile("" : "+r"(w));
+      p += (r & 1) ? bf16hi(w) : bf16lo(w);
+    }
+    const uint32_t vr = kv_row(kv, b, g, t0 + r);
+    if (vr == kInvalidRow) continue;
+    const uint16_t* v = kv.v + (int64_t)vr * kHeadDim;
+    for (int c = 0; c < 4; ++c) {
+      float o[32];
+      __syncwarp();
+      tmem_ld32(to + c * 32, o);
+      tmem_wait_ld();
+      tmem_loaded32(o);
+      if (seen >> r & 1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x[8];
+          unpack8(__ldg(reinterpret_cast<const uint4*>(v + c * 32) + e), x);
+#pragma unroll
+          for (int d = 0; d < 8; ++d) o[8 * e + d] += p * x[d];
+        }
+      }
+      __syncwarp();
+      tmem_st32(to + c * 32, o);
+    }
+    tmem_wait_st();
   }
 }
 
@@ -308,10 +446,11 @@ template <int QP, int PP>
 __global__ void __launch_bounds__(kTaThreads, 1)
     tree_decode_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ KvMaps maps) {
   using SH = TreeShape<QP, PP>;
-  constexpr int TT = SH::TT, NS = SH::kSlots;
+  constexpr int TT = SH::TT, KS = SH::kKSlots, VS = SH::kVSlots;
   extern __shared__ __align__(1024) unsigned char ta_smem[];
   unsigned char* qtile = ta_smem;
-  unsigned char* ring = ta_smem + SH::kQBytes;
+  unsigned char* kring = ta_smem + SH::kQBytes;
+  unsigned char* vring = kring + KS * SH::kSlotBytes;
   TreeCtl* ctl = reinterpret_cast<TreeCtl*>(ta_smem + kTaTiles);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.qv.hq / a.kv.hkv;
@@ -321,22 +460,28 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     return;
   }
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&ctl->full[i], 1);
-      mbar_init(&ctl->empty[i], 1);
+    for (int i = 0; i < SH::kKSlots; ++i) {
+      mbar_init(&ctl->k_full[i], 1);
+      mbar_init(&ctl->k_empty[i], 2);
+    }
+    for (int i = 0; i < SH::kVSlots; ++i) {
+      mbar_init(&ctl->v_full[i], 1);
+      mbar_init(&ctl->v_empty[i], 2);
     }
     mbar_init(&ctl->q_ready, 256);
-    mbar_init(&ctl->drain, 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&ctl->s_full[s], 1);
-      mbar_init(&ctl->p_ready[s], 128);
-      mbar_init(&ctl->o_done[s], 1);
+      for (int d = 0; d < 2; ++d) {
+        mbar_init(&ctl->s_full[s][d], 1);
+        mbar_init(&ctl->p_ready[s][d], 128);
+        mbar_init(&ctl->o_done[s][d], 1);
+      }
       mbar_init(&ctl->fixed[s], 128);
+      mbar_init(&ctl->drain[s], 1);
     }
     ctl->abort = 0;
     mbar_fence_init();
   }
-  if (warp == 9) {
+  if (warp == 10) {
     tmem_alloc(&ctl->tmem, 512);
     tmem_relinquish();
   }
@@ -391,143 +536,187 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   TreeWalk<SH> wk;
   wk.start(a, G, ctl->b0, ctl->off, share);
 
-  if (warp == 9) {
-    // ---- producer: K and V of every tile of every segment, in order, load n into slot n % NS
-    const int bp = a.kv.page_table == nullptr ? TT : min(TT, 1 << a.kv.page_shift);
-    uint32_t n = 0;
+  if (warp >= 10) {
+    // ---- producers: warp 10 loads K, warp 11 V, tile n of the share into slot n % slots of its ring.
+    // The TMA unit takes about 80 cycles for a box of 16 rows x 128 bytes, 25 bytes a cycle against
+    // the 23 that are an SM's part of the HBM rate, so little may stand between the boxes: the page
+    // numbers of 32 boxes are fetched and resolved at once, the next 32 while those are used.
+    const bool is_v = warp == 11;
+    const CUtensorMap* map = is_v ? &maps.v : &maps.k;
+    unsigned char* ring = is_v ? vring : kring;
+    uint64_t *full = is_v ? ctl->v_full : ctl->k_full, *empty = is_v ? ctl->v_empty : ctl->k_empty;
+    const uint32_t slots = is_v ? VS : KS;
+    // Pages of 8 or more tokens: boxes of `per` rows, one a lane; smaller pages: four rows a lane.
+    const bool paged = a.kv.page_table != nullptr, gather = paged && a.kv.page_shift < 3;
+    const int shift = paged ? a.kv.page_shift : 0, in_page = (1 << shift) - 1;
+    const int per = !paged ? TT : (gather ? 4 : min(TT, 1 << shift));
+    const int per_tile = TT / per, window = 32 / per_tile;   // boxes of a tile, tiles of 32 boxes
+    const int page_rows = a.kv.hkv << shift, no_row = (int)(a.kv.num_pages * page_rows);   // no_row: zeros arrive
+    const uint32_t num_pages = (uint32_t)a.kv.num_pages;
+    uint32_t slot = 0, round = 0, n = 0;
     for (; wk.live(); wk.next(a, G)) {
+      const int len = wk.s.len;
       // rows that no other unit reads are the first to leave L2
       const uint64_t pol = wk.s.mtiles == 1 ? l2_evict_first() : l2_evict_normal();
-      // this lane's rows of a tile: one box, or (small pages) four rows
-      auto coords = [&](int tile, int (&y)[4], uint32_t& bad) {
-        bad = 0;
-        const int per = bp >= 8 ? bp : 4;
+      const int32_t* table = a.kv.page_table + (int64_t)wk.b * a.kv.max_pages;
+      const int head_row = paged ? wk.g << shift : (wk.b * a.kv.hkv + wk.g) * a.kv.max_seq_len;
+      int page[4], y[4];
+      uint32_t bad = 0, any_bad = 0;
+      auto fetch = [&](int tile) {   // asks for the page numbers of this lane's rows of 32 boxes
         const int t = tile * TT + lane * per;
+        page[0] = paged && t < len ? __ldg(table + (t >> shift)) : 0;
+        if (gather) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[e] = 0;
-          if (e > 0 && bp >= 8) continue;
-          const int te = t + e;
-          if (lane * per >= TT || t >= wk.s.len) continue;
-          if (a.kv.page_table == nullptr) {
-            y[e] = (wk.b * a.kv.hkv + wk.g) * a.kv.max_seq_len + te;
-            continue;
-          }
-          const int32_t page = te < wk.s.len
-                                   ? __ldg(a.kv.page_table + (int64_t)wk.b * a.kv.max_pages + (te >> a.kv.page_shift)) : 0;
-          if (page < 0 || (int64_t)page >= a.kv.num_pages) {
-            bad |= 1u << e;
-            y[e] = (int)(a.kv.num_pages * a.kv.hkv << a.kv.page_shift);   // past the last row: zeros arrive
-          } else {
-            y[e] = (int)((((int64_t)page * a.kv.hkv + wk.g) << a.kv.page_shift) | (te & ((1 << a.kv.page_shift) - 1)));
-          }
+          for (int e = 1; e < 4; ++e) page[e] = t + e < len ? __ldg(table + ((t + e) >> shift)) : 0;
         }
       };
-      int y[4], y2[4];
-      uint32_t bad, bad2;
-      coords(wk.k0, y, bad);
-      for (int tile = wk.k0; tile < wk.k1; ++tile) {
-        if (tile + 1 < wk.k1) coords(tile + 1, y2, bad2);   // the page numbers of the next tile are under way
-        const int rows = min(TT, wk.s.len - tile * TT);
+      auto resolve = [&](int tile) {
+        const int t = tile * TT + lane * per;
+        if (!paged) {
+          y[0] = head_row + t;
+        } else {
+          bad = (uint32_t)page[0] >= num_pages;
+          y[0] = bad ? no_row : page[0] * page_rows + head_row + (t & in_page);
+          if (gather) {
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++n) {
-          const uint32_t slot = n % NS;
-          if (n >= NS) tree_wait_warp(&ctl->empty[slot], (n / NS - 1) & 1, ctl, a.status);
-          if (kv == 0) {
-            // rows of bad pages, as bits of the tile
-            const bool any = __any_sync(0xFFFFFFFFu, bad != 0);
-            uint32_t* marks = ctl->bad[(n >> 1) & 15];
-            if (lane < 4) marks[lane] = 0;
-            __syncwarp();
-            if (any) {
-              const int per = bp >= 8 ? bp : 4;
-              if (bad) flag_optional(a.status, TSD_DEV_BAD_PAGE);
-              for (int e = 0; e < per && lane * per < TT; ++e)
-                if (bad & (bp >= 8 ? 1u : 1u << e)) 
-                  atomicOr(&marks[(lane * per + e) >> 5], 1u << ((lane * per + e) & 31));
-              __syncwarp();
+            for (int e = 1; e < 4; ++e) {
+              const bool none = (uint32_t)page[e] >= num_pages;
+              bad |= (uint32_t)none << e;
+              y[e] = none ? no_row : page[e] * page_rows + head_row + ((t + e) & in_page);
             }
           }
-          tree_issue<TT>(kv ? &maps.v : &maps.k, ring + (size_t)slot * SH::kSlotBytes, &ctl->full[slot], y, bp, rows, lane,
-                         pol);
+          any_bad = __ballot_sync(0xFFFFFFFFu, bad != 0);
+          if (bad && !is_v) flag_optional(a.status, TSD_DEV_BAD_PAGE);
         }
+      };
+      fetch(wk.k0);
+      for (int tile = wk.k0, w = 0; tile < wk.k1; ++tile, ++n) {
+        if (w == 0) {
+          resolve(tile);
+          if (tile + window < wk.k1) fetch(tile + window);
+        }
+        const int box0 = w * per_tile, boxes = min(per_tile, (len - tile * TT + per - 1) / per);
+        if (++w == window) w = 0;
+        if (round > 0) tree_wait_warp(&empty[slot], (round - 1) & 1, ctl, a.status);
+        if (!is_v) {
+          uint32_t* marks = ctl->bad[n & 31];
+          if (lane < 2) marks[lane] = 0;
+          if (any_bad >> box0 & low_bits(per_tile)) {   // rows of bad pages, as bits of the tile
+            __syncwarp();
+            const int r0 = (lane - box0) * per;
+            if (lane >= box0 && r0 < TT)
+              for (int e = 0; e < per; ++e)
+                if (bad & (gather ? 1u << e : 1u)) atomicOr(&marks[(r0 + e) >> 5], 1u << ((r0 + e) & 31));
+          }
+          __syncwarp();
+        }
+        unsigned char* dst = ring + slot * SH::kSlotBytes;
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(boxes * per * 256));
+        // one thread issues: a TMA instruction with other operands in every lane is split up
+        if (gather) {
+          for (int i = 0; i < boxes; ++i) {
+            int yi[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = y2[e];
-        bad = bad2;
+            for (int e = 0; e < 4; ++e) yi[e] = __shfl_sync(0xFFFFFFFFu, y[e], box0 + i);
+            if (lane == 0) {
+              tma_gather4_hint(dst + i * 512, map, 0, yi, &full[slot], pol);
+              tma_gather4_hint(dst + TT * 128 + i * 512, map, 64, yi, &full[slot], pol);
+            }
+          }
+        } else {
+          for (int i = 0; i < boxes; ++i) {
+            const int yi = __shfl_sync(0xFFFFFFFFu, y[0], box0 + i);
+            if (lane == 0) {
+              tma_load_2d_hint(dst + i * per * 128, map, 0, yi, &full[slot], pol);
+              tma_load_2d_hint(dst + TT * 128 + i * per * 128, map, 64, yi, &full[slot], pol);
+            }
+          }
+        }
+        if (++slot == slots) {
+          slot = 0;
+          ++round;
+        }
       }
     }
-    // no copy may be in flight when the CTA ends
-    for (uint32_t i = n > NS ? n - NS : 0; i < n; ++i) tree_wait_warp(&ctl->full[i % NS], (i / NS) & 1, ctl, a.status);
+    // no copy may be in flight when the CTA ends: the fills of this round, then of the one before
+    for (uint32_t i = 0; i < slot; ++i) tree_wait_warp(&full[i], round & 1, ctl, a.status);
+    if (round > 0)
+      for (uint32_t i = slot; i < slots; ++i) tree_wait_warp(&full[i], (round - 1) & 1, ctl, a.status);
   }
-  else if (warp == 8) {
-    // ---- MMA issuer
+  else if (warp == 8 || warp == 9) {
+    // ---- MMA issuers: one thread for each stream.  A step's products are followed by the scores of the
+    // step after next, into the buffer that the products have just read (MMAs run in order).
     if (lane == 0) {
+      const int s = warp - 8;
       constexpr uint32_t idesc_s = umma_idesc_bf16_f32(128, TT), idesc_o = umma_idesc_bf16_f32_bmn(128, 128);
-      uint32_t loads = 0, done[2] = {0, 0}, fixes[2] = {0, 0}, segs = 0;
+      const uint64_t q_desc = sw128_desc(smem_u32(qtile), 1024), ring_k = sw128_desc(smem_u32(kring), 1024),
+                     ring_v = sw128_mn_desc(smem_u32(vring), TT * 128, 1024);
+      const uint32_t tm = tmem + s * 256;
+      uint32_t tiles_done = 0, done = 0, fixes = 0, segs = 0;
       for (; wk.live(); wk.next(a, G), ++segs) {
         const bool dual = wk.dual(G);
-        const int ntile = wk.k1 - wk.k0;
-        const int steps[2] = {dual ? ntile : (ntile + 1) / 2, dual ? ntile : ntile / 2};
+        const int ntile = wk.k1 - wk.k0, stride = dual ? 1 : 2, first = dual ? 0 : s;
+        const int steps = (ntile - first + stride - 1) / stride;
+        const uint64_t qd = q_desc + (dual && s ? 32768 >> 4 : 0);
         tree_wait(&ctl->q_ready, segs & 1, ctl, a.status);
         tc_fence_after_sync();
-        auto scores = [&](int s, int i) {
-          const uint32_t n = loads + 2 * (dual ? i : 2 * i + s), slot = n % NS;
-          tree_wait(&ctl->full[slot], (n / NS) & 1, ctl, a.status);
+        auto scores = [&](int i) {
+          const uint32_t n = tiles_done + first + stride * i, slot = n % KS, buf = (done + i) & 1;
+          tree_wait(&ctl->k_full[slot], (n / KS) & 1, ctl, a.status);
           tc_fence_after_sync();
-          const uint32_t kb = smem_u32(ring + (size_t)slot * SH::kSlotBytes);
-          const uint32_t qb = smem_u32(qtile) + (dual && s ? 32768u : 0u);
+          const uint64_t kd = ring_k + (uint64_t)(slot * (SH::kSlotBytes >> 4));
 #pragma unroll
-          for (int p = 0; p < QP; ++p)
+          for (int p = QP - 1; p >= 0; --p)   // the small parts first: every step rounds the sum so far
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-              umma_bf16(tmem + s * 256, sw128_desc(qb + p * 32768 + (ks >> 2) * 16384 + (ks & 3) * 32, 1024),
-                        sw128_desc(kb + (ks >> 2) * (TT * 128) + (ks & 3) * 32, 1024), idesc_s, p + ks > 0);
-          umma_commit(&ctl->s_full[s]);
-          if (!dual || s == 1) umma_commit(&ctl->empty[slot]);
+              umma_bf16(tm + buf * 64, qd + ((p * 32768 + (ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
+                        kd + (((ks >> 2) * (TT * 128) + (ks & 3) * 32) >> 4), idesc_s, p < QP - 1 || ks > 0);
+          umma_commit(&ctl->s_full[s][buf]);
+          umma_commit(&ctl->k_empty[slot]);   // expects both streams; a tile of one stream counts twice
+          if (!dual) umma_commit(&ctl->k_empty[slot]);
         };
-        for (int s = 0; s < 2; ++s)
-          if (steps[s] > 0) scores(s, 0);
-        for (int i = 0; i < steps[0]; ++i) {
-          for (int s = 0; s < 2; ++s) {
-            if (i >= steps[s]) continue;
-            const int at = dual ? i : 2 * i + s;
-            const uint32_t n = loads + 2 * at + 1, slot = n % NS;
-            tree_wait(&ctl->p_ready[s], (done[s] + i) & 1, ctl, a.status);
-            tree_wait(&ctl->full[slot], (n / NS) & 1, ctl, a.status);
-            tc_fence_after_sync();
-            const uint32_t vb = smem_u32(ring + (size_t)slot * SH::kSlotBytes);
+        if (steps > 0) scores(0);
+        if (steps > 1) scores(1);
+        for (int i = 0; i < steps; ++i) {
+          const int at = first + stride * i;
+          const uint32_t n = tiles_done + at, slot = n % VS, buf = (done + i) & 1;
+          tree_wait(&ctl->v_full[slot], (n / VS) & 1, ctl, a.status);
+          tree_wait(&ctl->p_ready[s][buf], ((done + i) >> 1) & 1, ctl, a.status);
+          tc_fence_after_sync();
+          const uint64_t vd = ring_v + (uint64_t)(slot * (SH::kSlotBytes >> 4));
+          const bool fresh = SH::kFlush ? i % (SH::kFlush ? SH::kFlush : 1) == 0 : i == 0;
 #pragma unroll
-            for (int p = 0; p < PP; ++p)
+          for (int p = PP - 1; p >= 0; --p)
 #pragma unroll
-              for (int ks = 0; ks < TT / 16; ++ks)
-                umma_bf16_ts(tmem + s * 256 + 128, tmem + s * 256 + p * (TT / 2) + ks * 8,
-                             sw128_mn_desc(vb + ks * 2048, TT * 128, 1024), idesc_o, i + p + ks > 0);
-            umma_commit(&ctl->o_done[s]);
-            if (!dual || s == 1) umma_commit(&ctl->empty[slot]);
-            if (i + 1 < steps[s]) {
-              if ((wk.k0 + at + 1) * TT > wk.s.base) {   // a special tile: P is read once more
-                tree_wait(&ctl->fixed[s], fixes[s]++ & 1, ctl, a.status);
-                tc_fence_after_sync();
-              }
-              scores(s, i + 1);
+            for (int ks = 0; ks < TT / 16; ++ks)
+              umma_bf16_ts(tm + 128, tm + buf * 64 + p * (TT / 2) + ks * 8, vd + (ks * 2048 >> 4), idesc_o,
+                           !fresh || p < PP - 1 || ks > 0);
+          umma_commit(&ctl->o_done[s][buf]);
+          umma_commit(&ctl->v_empty[slot]);
+          if (!dual) umma_commit(&ctl->v_empty[slot]);
+          if (i + 2 < steps) {
+            if ((wk.k0 + at + 1) * TT > wk.s.base) {   // a special tile: P is read once more
+              tree_wait(&ctl->fixed[s], fixes++ & 1, ctl, a.status);
+              tc_fence_after_sync();
             }
+            scores(i + 2);
           }
         }
-        loads += 2 * ntile;
-        done[0] += steps[0];
-        done[1] += steps[1];
+        tiles_done += ntile;
+        done += steps;
       }
       // no MMA may be in flight when tensor memory is freed
-      umma_commit(&ctl->drain);
-      if (!mbar_wait(&ctl->drain, 0)) flag_optional(a.status, TSD_DEV_TIMEOUT);
+      umma_commit(&ctl->drain[s]);
+      if (!mbar_wait(&ctl->drain[s], 0)) flag_optional(a.status, TSD_DEV_TIMEOUT);
     }
     __syncwarp();
-  } else {
+  } else if (warp < 8) {
     // ---- softmax: a list a thread
     const int s = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;   // this warp's tensor-memory lanes
-    const uint32_t tp = tmem + lanes + s * 256, to = tp + 128;  // S and P, O
+    const uint32_t tm = tmem + lanes + s * 256, to = tm + 128;  // S and P (two buffers), O
     const float scale = a.qv.sm_scale * 1.44269504088896340736f;   // base-2 units
+    float4* sums = a.sums + ((int64_t)blockIdx.x * 2 + s) * 32 * kTaRowsPerStream + row;   // kFlush: this list's sums
     uint32_t done = 0, tiles_done = 0;
     for (; wk.live(); wk.next(a, G)) {
       const TreeSeq& sq = wk.s;
@@ -580,78 +769,40 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       mbar_arrive(&ctl->q_ready);
 
       float m = -INFINITY, l = 0.f;
-      uint32_t vis[TT / 32], nf[4] = {0, 0, 0, 0};
-      // Adds to O the products of the rows of V that were zeroed for their infinities or NaNs, for
-      // the lists that see them.  The tile's P is still in tensor memory.
-      auto add_nonfinite = [&](int tile, uint32_t phase) {
-        if ((nf[0] | nf[1] | nf[2] | nf[3]) == 0 || !warp_live) return;
-        tree_wait_warp(&ctl->o_done[s], phase, ctl, a.status);
-        tc_fence_after_sync();
-        for (int r = 0; r < TT; ++r) {
-          if (!(nf[r >> 5] >> (r & 31) & 1)) continue;
-          float p = 0.f;
-          for (int part = 0; part < PP; ++part) {
-            uint32_t w = tmem_ld1(tp + part * (TT / 2) + (r >> 1));
-            tmem_wait_ld();
-            asm volatile("" : "+r"(w));
-            p += (r & 1) ? bf16hi(w) : bf16lo(w);
-          }
-          bool seen = false;
-#pragma unroll
-          for (int w = 0; w < TT / 32; ++w)
-            if ((r >> 5) == w) seen = vis[w] >> (r & 31) & 1;
-          const uint32_t vr = kv_row(a.kv, wk.b, wk.g, tile * TT + r);
-          if (vr == kInvalidRow) continue;
-          const uint16_t* v = a.kv.v + (int64_t)vr * kHeadDim;
-          for (int c = 0; c < 4; ++c) {
-            float o[32];
-            tmem_ld32(to + c * 32, o);
-            tmem_wait_ld();
-            tmem_loaded32(o);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float x[8];
-              unpack8(__ldg(reinterpret_cast<const uint4*>(v + c * 32) + e), x);
-#pragma unroll
-              for (int d = 0; d < 8; ++d)
-                if (seen) o[8 * e + d] += p * x[d];
-            }
-            __syncwarp();
-            tmem_st32(to + c * 32, o);
-          }
-          tmem_wait_st();
-        }
-        tc_fence_before_sync();
-      };
+      float m_sum = -INFINITY;   // reference of the sums moved to global memory; -inf: none yet
+      uint64_t seen = 0;         // the special tile's tokens that this list sees
       for (int i = 0; i < steps; ++i) {
         const int at = dual ? i : 2 * i + s, tile = wk.k0 + at;
-        const uint32_t phase = (done + i) & 1, num = tiles_done + at;
+        const uint32_t step = done + i, num = tiles_done + at;
         const bool special = (tile + 1) * TT > sq.base;
-        tree_wait_warp(&ctl->s_full[s], phase, ctl, a.status);
+        const uint32_t tp = tm + (step & 1) * 64;
+        if (SH::kFlush && i > 0 && i % (SH::kFlush ? SH::kFlush : 1) == 0 && warp_live) {
+          tree_wait_warp(&ctl->o_done[s][(step - 1) & 1], ((step - 1) >> 1) & 1, ctl, a.status);
+          tc_fence_after_sync();
+          tree_flush(to, sums, m_sum == -INFINITY ? 0.f : fast_exp2(m_sum - m), m_sum != -INFINITY, valid);
+          m_sum = m;
+        }
+        tree_wait_warp(&ctl->s_full[s][step & 1], (step >> 1) & 1, ctl, a.status);
         tc_fence_after_sync();
         if (warp_live) {
           float x[TT];
 #pragma unroll
-          for (int c = 0; c < TT / 32; ++c) tmem_ld32(tp + c * 32, x + 32 * c);
+          for (int c = 0; c < TT / 32; ++c) tmem_ld32(tp + 32 * c, x + 32 * c);
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < TT / 32; ++c) tmem_loaded32(x + 32 * c);
-          const volatile uint32_t* bad = ctl->bad[num & 15];
-          uint32_t bw[TT / 32], any_bad = 0;
+          const volatile uint32_t* marks = ctl->bad[num & 31];
+          uint64_t bad = marks[0];
+          if (TT > 32) bad |= (uint64_t)marks[1] << 32;
+          if (special || bad != 0) {
+            seen = valid ? tree_visible<TT>(a, sq, j, tile * TT) & ~bad : 0u;
 #pragma unroll
-          for (int w = 0; w < TT / 32; ++w) any_bad |= bw[w] = bad[w];
-          if (special || any_bad) {
-#pragma unroll
-            for (int w = 0; w < TT / 32; ++w) {
-              vis[w] = valid ? tree_visible(a, sq, j, tile * TT + 32 * w) & ~bw[w] : 0u;
-#pragma unroll
-              for (int c = 0; c < 32; ++c) x[32 * w + c] = vis[w] >> c & 1 ? x[32 * w + c] : -INFINITY;
-            }
+            for (int c = 0; c < TT; ++c) x[c] = seen >> c & 1 ? x[c] : -INFINITY;
           }
-          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float mx4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int c = 0; c < TT; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], x[c]);
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * scale;
+          for (int c = 4; c + 1 < TT; c += 2) mx4[(c >> 1) & 3] = max3(mx4[(c >> 1) & 3], x[c], x[c + 1]);
+          const float mx = max3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3])) * scale;
           if (i == 0) {
             m = mx;
           } else {
@@ -660,28 +811,23 @@ __global__ void __launch_bounds__(kTaThreads, 1)
               const float f = grow ? fast_exp2(m - mx) : 1.f;
               if (grow) m = mx;
               l *= f;
-              tree_wait_warp(&ctl->o_done[s], phase ^ 1, ctl, a.status);
+              tree_wait_warp(&ctl->o_done[s][(step - 1) & 1], ((step - 1) >> 1) & 1, ctl, a.status);
               tc_fence_after_sync();
-              for (int c = 0; c < 4; ++c) {
-                float o[32];
-                tmem_ld32(to + c * 32, o);
-                tmem_wait_ld();
-                tmem_loaded32(o);
-#pragma unroll
-                for (int d = 0; d < 32; ++d) o[d] *= f;
-                tmem_st32(to + c * 32, o);
-              }
+              tree_scale(to, f);
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;   // nothing seen yet: weights 0
-          float l4[4] = {0.f, 0.f, 0.f, 0.f};
+          const float2 scale2 = make_float2(scale, scale), ref2 = make_float2(-ref, -ref);
+          float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < TT / 32; ++c) {
             float* p = x + 32 * c;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              p[e] = fast_exp2(fmaf(p[e], scale, -ref));
-              l4[e & 3] += p[e];
+            for (int e = 0; e < 32; e += 2) {
+              const float2 z = __ffma2_rn(make_float2(p[e], p[e + 1]), scale2, ref2);
+              p[e] = fast_exp2(z.x);
+              p[e + 1] = fast_exp2(z.y);
+              l2[(e >> 1) & 1] = __fadd2_rn(l2[(e >> 1) & 1], make_float2(p[e], p[e + 1]));
             }
 #pragma unroll
             for (int part = 0; part < PP; ++part) {
@@ -697,65 +843,43 @@ __global__ void __launch_bounds__(kTaThreads, 1)
               tmem_st16(tp + part * (TT / 2) + 16 * c, w);
             }
           }
-          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          l2[0] = __fadd2_rn(l2[0], l2[1]);
+          l += l2[0].x + l2[0].y;
           tmem_wait_st();
         }
+        uint64_t odd = 0;
         if (special) {
-          // this tile's V in shared memory: rows behind the sequence and drafts' rows that are not
-          // finite become zeros
-          const uint32_t n = 2 * num + 1, slot = n % NS;
-          unsigned char* vt = ring + (size_t)slot * SH::kSlotBytes;
-          const int threads = dual ? 256 : 128, id = dual ? tid : row, bar = dual ? 1 : 2 + s;
-          uint32_t* found = ctl->nf[dual ? 0 : s];
-          tree_wait_warp(&ctl->full[slot], (n / NS) & 1, ctl, a.status);
-          named_sync(bar, threads);
-          if (id < 4) found[id] = 0;
-          named_sync(bar, threads);
-          for (int e = id; e < TT * 16; e += threads) {
-            const int r = e >> 4, ch = e & 15, t = tile * TT + r;
-            if (t < sq.base) continue;
-            uint4* p = reinterpret_cast<uint4*>(vt + (ch >> 3) * (TT * 128) + sw128(r, ch & 7));
-            if (t >= sq.len) {
-              *p = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            const uint4 v = *p;
-            uint32_t odd = 0;   // an exponent of all ones
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t u = w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
-              odd |= ((u & 0x7F80u) == 0x7F80u) | ((u & 0x7F800000u) == 0x7F800000u);
-            }
-            if (odd) atomicOr(&found[r >> 5], 1u << (r & 31));
-          }
-          named_sync(bar, threads);
-          uint32_t any = 0;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) any |= nf[w] = found[w];
-          if (any) {
-            for (int e = id; e < TT * 16; e += threads) {
-              const int r = e >> 4, ch = e & 15;
-              if (found[r >> 5] >> (r & 31) & 1)
-                *reinterpret_cast<uint4*>(vt + (ch >> 3) * (TT * 128) + sw128(r, ch & 7)) = make_uint4(0, 0, 0, 0);
-            }
-          }
-          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-          if (dual) named_sync(bar, threads);   // the other stream's products read these rows too
+          const uint32_t slot = num % VS;
+          tree_wait_warp(&ctl->v_full[slot], (num / VS) & 1, ctl, a.status);
+          odd = tree_clean_v<TT>(vring + (size_t)slot * SH::kSlotBytes, ctl->nf[dual ? 0 : s], tile * TT, sq.base, sq.len,
+                                 dual ? tid : row, dual ? 256 : 128, dual ? 1 : 2 + s);
         }
         tc_fence_before_sync();
-        mbar_arrive(&ctl->p_ready[s]);
+        mbar_arrive(&ctl->p_ready[s][step & 1]);
         if (special) {
-          add_nonfinite(tile, phase);
-          if (i + 1 < steps) mbar_arrive(&ctl->fixed[s]);
+          if (odd != 0 && warp_live) {
+            tree_wait_warp(&ctl->o_done[s][step & 1], (step >> 1) & 1, ctl, a.status);
+            tc_fence_after_sync();
+            tree_add_nonfinite<TT, PP>(a.kv, wk.b, wk.g, tile * TT, odd, seen, tp, to);
+            tc_fence_before_sync();
+          }
+          if (i + 2 < steps) mbar_arrive(&ctl->fixed[s]);
         }
       }
-      if (steps > 0) tree_wait_warp(&ctl->o_done[s], (done + steps - 1) & 1, ctl, a.status);
+      if (steps > 0) {
+        const uint32_t last = done + steps - 1;
+        tree_wait_warp(&ctl->o_done[s][last & 1], (last >> 1) & 1, ctl, a.status);
+      }
+      tc_fence_after_sync();
       done += steps;
       tiles_done += ntile;
 
       // ---- the segment's state: O / l where the unit is whole, else a partial state
       float w0 = 1.f, w1 = 0.f;
       bool two = false;
+      if (SH::kFlush && m_sum != -INFINITY && warp_live) {   // the sums in global memory come on top
+        tree_unflush(to, sums, fast_exp2(m_sum - m), valid);
+      }
       if (!dual) {
         ctl->ml[s][row] = make_float2(m, l);
         tc_fence_before_sync();
@@ -824,7 +948,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     }
   }
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 10) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
@@ -893,17 +1017,18 @@ __global__ void __launch_bounds__(kTgThreads) tree_merge_kernel(const __grid_con
 }
 
 struct TreeLayout {
-  size_t line, ml, acc, total;
+  size_t line, ml, acc, sums, total;
   int part_rows;
 };
-static TreeLayout tree_layout(const Shapes& sh, int ctas, bool q_f32) {
+static TreeLayout tree_layout(const Shapes& sh, int ctas, bool q_f32, bool out_f32) {
   TreeLayout l;
   const int64_t lists = (sh.group * sh.max_tokens + 31) / 32 * 32, rows = q_f32 ? 128 : 256;
   l.part_rows = (int)(lists < rows ? lists : rows);
   l.line = 0;
   l.ml = align256((size_t)(1 + sh.batch) * sizeof(int64_t));
   l.acc = l.ml + align256((size_t)2 * ctas * l.part_rows * sizeof(float2));
-  l.total = l.acc + align256((size_t)2 * ctas * 32 * l.part_rows * sizeof(float4));
+  l.sums = l.acc + align256((size_t)2 * ctas * 32 * l.part_rows * sizeof(float4));
+  l.total = l.sums + (out_f32 ? (size_t)2 * ctas * 32 * kTaRowsPerStream * sizeof(float4) : 0);
   return l;
 }
 
@@ -953,10 +1078,11 @@ tsd_status tsd_tree_mask(int32_t batch, const int32_t* q_indptr, int32_t num_tok
   return cuda_status(cudaGetLastError());
 }
 
-size_t tsd_tree_decode_workspace_size(const tsd_kv_cache* cache, const tsd_queries* queries) {
+size_t tsd_tree_decode_workspace_size(const tsd_kv_cache* cache, const tsd_queries* queries, int32_t out_dtype) {
   Shapes sh;
   if (sizes_for(cache, queries, &sh) != TSD_OK || sh.max_tokens > kMaxTree) return 0;
-  return tree_layout(sh, current_sm_count(), queries->q_dtype == TSD_F32).total;
+  if (out_dtype != TSD_BF16 && out_dtype != TSD_F32) return 0;
+  return tree_layout(sh, current_sm_count(), queries->q_dtype == TSD_F32, out_dtype == TSD_F32).total;
 }
 
 tsd_status tsd_tree_decode(const tsd_kv_cache* cache, const tsd_queries* queries, const uint32_t* mask, void* out,
@@ -972,7 +1098,7 @@ tsd_status tsd_tree_decode(const tsd_kv_cache* cache, const tsd_queries* queries
   if (out_dtype != TSD_BF16 && out_dtype != TSD_F32) return TSD_ERR_UNSUPPORTED;
   if (sh.max_tokens > kMaxTree) return TSD_ERR_UNSUPPORTED;
   a.ctas = current_sm_count();
-  const TreeLayout l = tree_layout(sh, a.ctas, a.qv.q_f32);
+  const TreeLayout l = tree_layout(sh, a.ctas, a.qv.q_f32, out_dtype == TSD_F32);
   if (ws_bytes < l.total) return TSD_ERR_WORKSPACE_TOO_SMALL;
   const int64_t groups = (sh.group * sh.max_tokens + 31) / 32;
   if (sh.batch * sh.hkv * groups > 0x7fffffffLL) return TSD_ERR_UNSUPPORTED;
@@ -987,9 +1113,9 @@ tsd_status tsd_tree_decode(const tsd_kv_cache* cache, const tsd_queries* queries
   a.line = reinterpret_cast<int64_t*>(w + l.line);
   a.part_ml = reinterpret_cast<float2*>(w + l.ml);
   a.part_acc = reinterpret_cast<float4*>(w + l.acc);
+  a.sums = reinterpret_cast<float4*>(w + l.sums);
   KvMaps maps;
-  const int tt = a.qv.q_f32 || a.out_f32 ? 64 : 128;
-  st = make_kv_maps(cache, &maps, tt, true);
+  st = make_kv_maps(cache, &maps, a.out_f32 ? TreeShape<1, 3>::TT : TreeShape<1, 1>::TT, true);
   if (st != TSD_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;

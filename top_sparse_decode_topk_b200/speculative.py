@@ -224,10 +224,10 @@ def tree_decode(cache: KVCache, queries: Queries, mask=None, out=None, out_dtype
             lse = None
         elif tuple(lse.shape) != (T, Hq) or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous float32 [T, Hq] tensor on the cache's device")
-        nbytes = lib.tsd_tree_decode_workspace_size(ctypes.byref(cs), ctypes.byref(qs))
+        odt = TSD_BF16 if out.dtype == torch.bfloat16 else TSD_F32
+        nbytes = lib.tsd_tree_decode_workspace_size(ctypes.byref(cs), ctypes.byref(qs), odt)
         ws, sp = _scratch(workspace, nbytes, ("tree_decode",) + _shape_key(cache, queries), dev, call, status)
-        _check(lib.tsd_tree_decode(ctypes.byref(cs), ctypes.byref(qs), mp, out.data_ptr(),
-                                   TSD_BF16 if out.dtype == torch.bfloat16 else TSD_F32,
+        _check(lib.tsd_tree_decode(ctypes.byref(cs), ctypes.byref(qs), mp, out.data_ptr(), odt,
                                    None if lse is None else lse.data_ptr(), ws[0], nbytes, sp, call.ptr),
                "tsd_tree_decode")
     return out, lse
