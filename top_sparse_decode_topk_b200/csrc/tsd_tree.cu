@@ -130,7 +130,7 @@ struct TreeArgs {
   int32_t out_f32;
   float* lse;
   uint32_t* status;
-  int64_t* line;       // [0] tiles in all, [1 + b] first tile of sequence b
+  int32_t* line;       // [0] tiles in all, [1 + b] first tile of sequence b
   float2* part_ml;     // [2 * CTAs][part_rows] (maximum, sum), base-2 units
   float4* part_acc;    // [2 * CTAs][32][part_rows] four dims of an unnormalised row
   float4* sums;        // [CTAs][2][32][128] sums of a stream's products (fp32 outputs)
@@ -185,28 +185,37 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, int G, boo
   return s;
 }
 
-// CTA whose share holds tile x of `total` (CTA c starts at floor(total c / C)).
-__device__ __forceinline__ int tree_owner(int64_t x, int64_t total, int64_t C) { return (int)(((x + 1) * C - 1) / total); }
+// The line of `total` tiles cut into shares for C CTAs (C <= total): the first total % C shares have
+// one tile more than the others.
+struct TreeShares {
+  int q, r;
+  __device__ __forceinline__ TreeShares(int total, int C) : q(total / C), r(total % C) {}
+  __device__ __forceinline__ int begin(int c) const { return c * q + min(c, r); }
+  __device__ __forceinline__ int owner(int x) const {   // the CTA whose share holds tile x
+    const int big = r * (q + 1);
+    return x < big ? x / (q + 1) : r + (x - big) / q;
+  }
+};
 
 // The segments of a CTA's share, in order; every warp role walks them by itself.
 template <class SH>
 struct TreeWalk {
   TreeSeq s;
   int b, g, mt, k0, k1;   // segment: tiles [k0, k1) of unit (b, g, mt)
-  int64_t left;           // tiles of the share from k0 on
+  int left;               // tiles of the share from k0 on
 
-  __device__ __forceinline__ void start(const TreeArgs& a, int G, int b0, int64_t off, int64_t share) {
+  __device__ __forceinline__ void start(const TreeArgs& a, int G, int b0, int off, int share) {
     b = b0;
     left = share;
     if (left <= 0) return;
     s = tree_seq<SH>(a, b, G, false);
-    const int64_t unit = off / s.tiles;
-    g = (int)(unit / s.mtiles);
-    mt = (int)(unit % s.mtiles);
-    k0 = (int)(off - unit * s.tiles);
+    const int unit = off / s.tiles;
+    g = unit / s.mtiles;
+    mt = unit % s.mtiles;
+    k0 = off - unit * s.tiles;
     cut();
   }
-  __device__ __forceinline__ void cut() { k1 = (int)min((int64_t)s.tiles, k0 + left); }
+  __device__ __forceinline__ void cut() { k1 = min(s.tiles, k0 + left); }
   __device__ __forceinline__ bool live() const { return left > 0; }
   __device__ __forceinline__ void next(const TreeArgs& a, int G) {
     left -= k1 - k0;
@@ -216,7 +225,9 @@ struct TreeWalk {
       mt = 0;
       if (++g == a.kv.hkv) {
         g = 0;
-        do s = tree_seq<SH>(a, ++b, G, false); while (s.tiles == 0 || s.mtiles == 0);
+#pragma unroll 1
+        do s = tree_seq<SH>(a, ++b, G, false);
+        while (s.tiles == 0 || s.mtiles == 0);
       }
     }
     cut();
@@ -238,27 +249,25 @@ struct TreeCtl {
   // Rows with a bad page of tile m (counted over the CTA's share), at m % 32: K is loaded at most
   // 4 (two steps of two streams) + kKSlots <= 12 tiles ahead of the softmax.
   uint32_t bad[32][2];
-  int64_t scan[10];
-  int64_t total, off;
-  int b0;
+  int scan[kTaThreads / 32], off, b0;
   float2 ml[2][kTaRowsPerStream];
 };
 static_assert(sizeof(TreeCtl) <= kTaSmem - kTaTiles, "control block");
 
-// Bounded wait that gives way to `abort`.
+// Bounded wait that gives way to `abort`: up to 2^20 tries of up to a microsecond each.  Counted, not
+// timed, to keep the code small: the kernel's waits are many, and an instruction cache miss costs
+// a warp some hundred cycles.
 __device__ __forceinline__ void tree_wait(uint64_t* bar, uint32_t parity, TreeCtl* c, uint32_t* status) {
-  if (mbar_try_wait(bar, parity)) return;
-  const long long t0 = clock64();
-  while (!mbar_try_wait_suspend(bar, parity, 20000u)) {
+#pragma unroll 1
+  for (uint32_t tries = 0; !mbar_try_wait_suspend(bar, parity, 1000u);) {
     if (*reinterpret_cast<volatile uint32_t*>(&c->abort)) return;
-    if (clock64() - t0 > kWaitCycles) {
+    if (++tries == 1u << 20) {
       atomicOr(&c->abort, 1u);
       flag_optional(status, TSD_DEV_TIMEOUT);
       return;
     }
   }
 }
-
 // The same by all lanes of a warp, converged again behind it (as .aligned instructions need).
 __device__ __forceinline__ void tree_wait_warp(uint64_t* bar, uint32_t parity, TreeCtl* c, uint32_t* status) {
   tree_wait(bar, parity, c, status);
@@ -309,6 +318,7 @@ __device__ __noinline__ uint64_t tree_visible(const TreeArgs& a, TreeSeq s, int 
 
 // O of this warp's lists times f.
 __device__ __noinline__ void tree_scale(uint32_t to, float f) {
+#pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     float o[32];
     tmem_ld32(to + c * 32, o);
@@ -323,6 +333,7 @@ __device__ __noinline__ void tree_scale(uint32_t to, float f) {
 
 // sums = sums * f + O (sums are taken as 0 when !have): this list's column of [32][128] float4.
 __device__ __noinline__ void tree_flush(uint32_t to, float4* sums, float f, bool have, bool valid) {
+#pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     float o[32];
     __syncwarp();
@@ -342,6 +353,7 @@ __device__ __noinline__ void tree_flush(uint32_t to, float4* sums, float f, bool
 
 // O += sums * f.
 __device__ __noinline__ void tree_unflush(uint32_t to, const float4* sums, float f, bool valid) {
+#pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     float o[32];
     __syncwarp();
@@ -372,6 +384,7 @@ __device__ __noinline__ uint64_t tree_clean_v(unsigned char* vt, uint32_t* found
   named_sync(bar, threads);
   if (id < 2) found[id] = 0;
   named_sync(bar, threads);
+#pragma unroll 1
   for (int e = id; e < TT * 16; e += threads) {
     const int r = e >> 4, ch = e & 15, t = t0 + r;
     if (t < base) continue;
@@ -392,6 +405,7 @@ __device__ __noinline__ uint64_t tree_clean_v(unsigned char* vt, uint32_t* found
   named_sync(bar, threads);
   const uint64_t any = (uint64_t)found[1] << 32 | found[0];
   if (any) {
+#pragma unroll 1
     for (int e = id; e < TT * 16; e += threads) {
       const int r = e >> 4, ch = e & 15;
       if (any >> r & 1)
@@ -411,6 +425,7 @@ __device__ __noinline__ void tree_add_nonfinite(const KvView& kv, int b, int g, 
   for (; rows != 0; rows &= rows - 1) {
     const int r = __ffsll((long long)rows) - 1;
     float p = 0.f;
+#pragma unroll 1
     for (int part = 0; part < PP; ++part) {
       uint32_t w = tmem_ld1(tp + part * (TT / 2) + (r >> 1));
       tmem_wait_ld();
@@ -420,6 +435,7 @@ __device__ __noinline__ void tree_add_nonfinite(const KvView& kv, int b, int g, 
     const uint32_t vr = kv_row(kv, b, g, t0 + r);
     if (vr == kInvalidRow) continue;
     const uint16_t* v = kv.v + (int64_t)vr * kHeadDim;
+#pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       float o[32];
       __syncwarp();
@@ -487,33 +503,33 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   }
   // The line of all units' tiles: running sums over the sequences, then the sequence this CTA's
   // share starts in.
-  int64_t total = 0;
+  int total = 0, begin = -1, share = 0;
+#pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
-    int64_t run = 0;
-    const int64_t C = total > 0 ? min((int64_t)a.ctas, total) : 1;
-    const int64_t begin = total * min((int64_t)blockIdx.x, C) / C;
+    int run = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < a.kv.batch; b0 += kTaThreads) {
       const int b = b0 + tid;
-      int64_t cost = 0;
+      int cost = 0;
       if (b < a.kv.batch) {
         const TreeSeq s = tree_seq<SH>(a, b, G, pass == 0 && blockIdx.x == 0);
-        cost = (int64_t)s.mtiles * s.tiles * a.kv.hkv;
+        cost = s.mtiles * s.tiles * a.kv.hkv;
       }
-      int64_t x = cost;
+      int x = cost;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
         if (lane >= o) x += y;
       }
       __syncthreads();
       if (lane == 31) ctl->scan[warp] = x;
       __syncthreads();
-      int64_t before = run;
+      int before = run + x - cost;
+#pragma unroll 1
       for (int w = 0; w < kTaThreads / 32; ++w) {
         if (w < warp) before += ctl->scan[w];
         run += ctl->scan[w];
       }
-      before += x - cost;
       if (pass == 0) {
         if (blockIdx.x == 0 && b < a.kv.batch) a.line[1 + b] = before;
       } else if (begin >= before && begin < before + cost) {
@@ -521,18 +537,21 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         ctl->off = begin - before;
       }
     }
-    if (pass == 0) total = run;
+    if (pass == 0) {
+      total = run;
+      const int C = min(a.ctas, total);
+      if ((int)blockIdx.x < C) {
+        const TreeShares shares(total, C);
+        begin = shares.begin(blockIdx.x);
+        share = shares.begin(blockIdx.x + 1) - begin;
+      }
+    }
   }
   if (blockIdx.x == 0 && tid == 0) a.line[0] = total;
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = ctl->tmem;
-  int64_t share = 0;
-  if (total > 0) {
-    const int64_t C = min((int64_t)a.ctas, total);
-    if (blockIdx.x < C) share = total * (blockIdx.x + 1) / C - total * blockIdx.x / C;
-  }
   TreeWalk<SH> wk;
   wk.start(a, G, ctl->b0, ctl->off, share);
 
@@ -554,6 +573,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const int page_rows = a.kv.hkv << shift, no_row = (int)(a.kv.num_pages * page_rows);   // no_row: zeros arrive
     const uint32_t num_pages = (uint32_t)a.kv.num_pages;
     uint32_t slot = 0, round = 0, n = 0;
+#pragma unroll 1
     for (; wk.live(); wk.next(a, G)) {
       const int len = wk.s.len;
       // rows that no other unit reads are the first to leave L2
@@ -590,6 +610,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
       };
       fetch(wk.k0);
+#pragma unroll 1
       for (int tile = wk.k0, w = 0; tile < wk.k1; ++tile, ++n) {
         if (w == 0) {
           resolve(tile);
@@ -605,6 +626,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             __syncwarp();
             const int r0 = (lane - box0) * per;
             if (lane >= box0 && r0 < TT)
+#pragma unroll 1
               for (int e = 0; e < per; ++e)
                 if (bad & (gather ? 1u << e : 1u)) atomicOr(&marks[(r0 + e) >> 5], 1u << ((r0 + e) & 31));
           }
@@ -614,6 +636,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(boxes * per * 256));
         // one thread issues: a TMA instruction with other operands in every lane is split up
         if (gather) {
+#pragma unroll 1
           for (int i = 0; i < boxes; ++i) {
             int yi[4];
 #pragma unroll
@@ -624,6 +647,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             }
           }
         } else {
+#pragma unroll 1
           for (int i = 0; i < boxes; ++i) {
             const int yi = __shfl_sync(0xFFFFFFFFu, y[0], box0 + i);
             if (lane == 0) {
@@ -639,8 +663,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       }
     }
     // no copy may be in flight when the CTA ends: the fills of this round, then of the one before
+#pragma unroll 1
     for (uint32_t i = 0; i < slot; ++i) tree_wait_warp(&full[i], round & 1, ctl, a.status);
     if (round > 0)
+#pragma unroll 1
       for (uint32_t i = slot; i < slots; ++i) tree_wait_warp(&full[i], (round - 1) & 1, ctl, a.status);
   }
   else if (warp == 8 || warp == 9) {
@@ -653,6 +679,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                      ring_v = sw128_mn_desc(smem_u32(vring), TT * 128, 1024);
       const uint32_t tm = tmem + s * 256;
       uint32_t tiles_done = 0, done = 0, fixes = 0, segs = 0;
+#pragma unroll 1
       for (; wk.live(); wk.next(a, G), ++segs) {
         const bool dual = wk.dual(G);
         const int ntile = wk.k1 - wk.k0, stride = dual ? 1 : 2, first = dual ? 0 : s;
@@ -675,27 +702,28 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           umma_commit(&ctl->k_empty[slot]);   // expects both streams; a tile of one stream counts twice
           if (!dual) umma_commit(&ctl->k_empty[slot]);
         };
-        if (steps > 0) scores(0);
-        if (steps > 1) scores(1);
-        for (int i = 0; i < steps; ++i) {
+#pragma unroll 1
+        for (int i = -2; i < steps; ++i) {
           const int at = first + stride * i;
-          const uint32_t n = tiles_done + at, slot = n % VS, buf = (done + i) & 1;
-          tree_wait(&ctl->v_full[slot], (n / VS) & 1, ctl, a.status);
-          tree_wait(&ctl->p_ready[s][buf], ((done + i) >> 1) & 1, ctl, a.status);
-          tc_fence_after_sync();
-          const uint64_t vd = ring_v + (uint64_t)(slot * (SH::kSlotBytes >> 4));
-          const bool fresh = SH::kFlush ? i % (SH::kFlush ? SH::kFlush : 1) == 0 : i == 0;
+          if (i >= 0) {
+            const uint32_t n = tiles_done + at, slot = n % VS, buf = (done + i) & 1;
+            tree_wait(&ctl->v_full[slot], (n / VS) & 1, ctl, a.status);
+            tree_wait(&ctl->p_ready[s][buf], ((done + i) >> 1) & 1, ctl, a.status);
+            tc_fence_after_sync();
+            const uint64_t vd = ring_v + (uint64_t)(slot * (SH::kSlotBytes >> 4));
+            const bool fresh = SH::kFlush ? i % (SH::kFlush ? SH::kFlush : 1) == 0 : i == 0;
 #pragma unroll
-          for (int p = PP - 1; p >= 0; --p)
+            for (int p = PP - 1; p >= 0; --p)
 #pragma unroll
-            for (int ks = 0; ks < TT / 16; ++ks)
-              umma_bf16_ts(tm + 128, tm + buf * 64 + p * (TT / 2) + ks * 8, vd + (ks * 2048 >> 4), idesc_o,
-                           !fresh || p < PP - 1 || ks > 0);
-          umma_commit(&ctl->o_done[s][buf]);
-          umma_commit(&ctl->v_empty[slot]);
-          if (!dual) umma_commit(&ctl->v_empty[slot]);
+              for (int ks = 0; ks < TT / 16; ++ks)
+                umma_bf16_ts(tm + 128, tm + buf * 64 + p * (TT / 2) + ks * 8, vd + (ks * 2048 >> 4), idesc_o,
+                             !fresh || p < PP - 1 || ks > 0);
+            umma_commit(&ctl->o_done[s][buf]);
+            umma_commit(&ctl->v_empty[slot]);
+            if (!dual) umma_commit(&ctl->v_empty[slot]);
+          }
           if (i + 2 < steps) {
-            if ((wk.k0 + at + 1) * TT > wk.s.base) {   // a special tile: P is read once more
+            if (i >= 0 && (wk.k0 + at + 1) * TT > wk.s.base) {   // a special tile: P is read once more
               tree_wait(&ctl->fixed[s], fixes++ & 1, ctl, a.status);
               tc_fence_after_sync();
             }
@@ -718,6 +746,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const float scale = a.qv.sm_scale * 1.44269504088896340736f;   // base-2 units
     float4* sums = a.sums + ((int64_t)blockIdx.x * 2 + s) * 32 * kTaRowsPerStream + row;   // kFlush: this list's sums
     uint32_t done = 0, tiles_done = 0;
+#pragma unroll 1
     for (; wk.live(); wk.next(a, G)) {
       const TreeSeq& sq = wk.s;
       const bool dual = wk.dual(G);
@@ -732,6 +761,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       {
         unsigned char* q0 = qtile + (dual && s ? 32768 : 0);
         const int threads = dual ? 128 : 256, id = dual ? row : tid;
+#pragma unroll 1
         for (int i = id; i < 128 * 16; i += threads) {
           const int r = i >> 4, ch = i & 15, ls = first + r;
           uint4 part[3];
@@ -771,6 +801,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       float m = -INFINITY, l = 0.f;
       float m_sum = -INFINITY;   // reference of the sums moved to global memory; -inf: none yet
       uint64_t seen = 0;         // the special tile's tokens that this list sees
+#pragma unroll 1
       for (int i = 0; i < steps; ++i) {
         const int at = dual ? i : 2 * i + s, tile = wk.k0 + at;
         const uint32_t step = done + i, num = tiles_done + at;
@@ -910,6 +941,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             a.part_ml[slot * a.part_rows + prow] = make_float2(m, l);
           }
         }
+#pragma unroll 1
         for (int c = c0; c < c1; ++c) {
           float o[32], o2[32];
           __syncwarp();
@@ -969,10 +1001,10 @@ __global__ void __launch_bounds__(kTgThreads) tree_merge_kernel(const __grid_con
   const int lists = sq.n * G;
   pdl_wait();
   if (rg * 32 >= lists) return;
-  const int64_t total = a.line[0], C = min((int64_t)a.ctas, total);
-  const int mt = rg * 32 / SH::kRows;
-  const int64_t u0 = a.line[1 + b] + ((int64_t)g * sq.mtiles + mt) * sq.tiles;
-  const int c0 = tree_owner(u0, total, C), c1 = tree_owner(u0 + sq.tiles - 1, total, C);
+  const int total = a.line[0];
+  const TreeShares shares(total, min(a.ctas, total));
+  const int mt = rg * 32 / SH::kRows, u0 = a.line[1 + b] + (g * sq.mtiles + mt) * sq.tiles;
+  const int c0 = shares.owner(u0), c1 = shares.owner(u0 + sq.tiles - 1);
   if (c0 == c1) return;   // written directly
   const int list = rg * 32 + lane, prow = list - mt * SH::kRows;
   if (list >= lists) return;
@@ -1025,7 +1057,7 @@ static TreeLayout tree_layout(const Shapes& sh, int ctas, bool q_f32, bool out_f
   const int64_t lists = (sh.group * sh.max_tokens + 31) / 32 * 32, rows = q_f32 ? 128 : 256;
   l.part_rows = (int)(lists < rows ? lists : rows);
   l.line = 0;
-  l.ml = align256((size_t)(1 + sh.batch) * sizeof(int64_t));
+  l.ml = align256((size_t)(1 + sh.batch) * sizeof(int32_t));
   l.acc = l.ml + align256((size_t)2 * ctas * l.part_rows * sizeof(float2));
   l.sums = l.acc + align256((size_t)2 * ctas * 32 * l.part_rows * sizeof(float4));
   l.total = l.sums + (out_f32 ? (size_t)2 * ctas * 32 * kTaRowsPerStream * sizeof(float4) : 0);
@@ -1101,7 +1133,8 @@ tsd_status tsd_tree_decode(const tsd_kv_cache* cache, const tsd_queries* queries
   const TreeLayout l = tree_layout(sh, a.ctas, a.qv.q_f32, out_dtype == TSD_F32);
   if (ws_bytes < l.total) return TSD_ERR_WORKSPACE_TOO_SMALL;
   const int64_t groups = (sh.group * sh.max_tokens + 31) / 32;
-  if (sh.batch * sh.hkv * groups > 0x7fffffffLL) return TSD_ERR_UNSUPPORTED;
+  // the line of tiles and the merge's grid are counted in 32 bits
+  if ((double)sh.batch * sh.hkv * groups * ((double)sh.max_seq_len / 32 + 1) >= 2147483647.0) return TSD_ERR_UNSUPPORTED;
   a.mask = mask;
   a.words = (int)(sh.max_tokens + 31) / 32;
   a.part_rows = l.part_rows;
@@ -1110,7 +1143,7 @@ tsd_status tsd_tree_decode(const tsd_kv_cache* cache, const tsd_queries* queries
   a.lse = lse;
   a.status = status;
   char* w = static_cast<char*>(ws);
-  a.line = reinterpret_cast<int64_t*>(w + l.line);
+  a.line = reinterpret_cast<int32_t*>(w + l.line);
   a.part_ml = reinterpret_cast<float2*>(w + l.ml);
   a.part_acc = reinterpret_cast<float4*>(w + l.acc);
   a.sums = reinterpret_cast<float4*>(w + l.sums);
