@@ -137,7 +137,8 @@ struct TreeArgs {
   int32_t ctas;
 };
 
-constexpr int kTaThreads = 384;
+constexpr int kTaThreads = 512;
+constexpr int kTaSoftmaxRegs = 168, kTaOtherRegs = 88;
 constexpr int kTaRowsPerStream = 128;
 constexpr int kTaTiles = 229376;               // Q tiles and the ring
 constexpr size_t kTaSmem = kTaTiles + 3072;    // then barriers and scratch: all of an SM's shared memory
@@ -272,6 +273,15 @@ __device__ __forceinline__ void tree_wait(uint64_t* bar, uint32_t parity, TreeCt
 __device__ __forceinline__ void tree_wait_warp(uint64_t* bar, uint32_t parity, TreeCtl* c, uint32_t* status) {
   tree_wait(bar, parity, c, status);
   __syncwarp();
+}
+
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
 __device__ __forceinline__ void named_sync(int id, int threads) {
@@ -552,193 +562,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = ctl->tmem;
-  TreeWalk<SH> wk;
-  wk.start(a, G, ctl->b0, ctl->off, share);
-
-  if (warp >= 10) {
-    // ---- producers: warp 10 loads K, warp 11 V, tile n of the share into slot n % slots of its ring.
-    // The TMA unit takes about 80 cycles for a box of 16 rows x 128 bytes, 25 bytes a cycle against
-    // the 23 that are an SM's part of the HBM rate, so little may stand between the boxes: the page
-    // numbers of 32 boxes are fetched and resolved at once, the next 32 while those are used.
-    const bool is_v = warp == 11;
-    const CUtensorMap* map = is_v ? &maps.v : &maps.k;
-    unsigned char* ring = is_v ? vring : kring;
-    uint64_t *full = is_v ? ctl->v_full : ctl->k_full, *empty = is_v ? ctl->v_empty : ctl->k_empty;
-    const uint32_t slots = is_v ? VS : KS;
-    // Pages of 8 or more tokens: boxes of `per` rows, one a lane; smaller pages: four rows a lane.
-    const bool paged = a.kv.page_table != nullptr, gather = paged && a.kv.page_shift < 3;
-    const int shift = paged ? a.kv.page_shift : 0, in_page = (1 << shift) - 1;
-    const int per = !paged ? TT : (gather ? 4 : min(TT, 1 << shift));
-    const int per_tile = TT / per, window = 32 / per_tile;   // boxes of a tile, tiles of 32 boxes
-    const int page_rows = a.kv.hkv << shift, no_row = (int)(a.kv.num_pages * page_rows);   // no_row: zeros arrive
-    const uint32_t num_pages = (uint32_t)a.kv.num_pages;
-    uint32_t slot = 0, round = 0, n = 0;
-#pragma unroll 1
-    for (; wk.live(); wk.next(a, G)) {
-      const int len = wk.s.len;
-      // rows that no other unit reads are the first to leave L2
-      const uint64_t pol = wk.s.mtiles == 1 ? l2_evict_first() : l2_evict_normal();
-      const int32_t* table = a.kv.page_table + (int64_t)wk.b * a.kv.max_pages;
-      const int head_row = paged ? wk.g << shift : (wk.b * a.kv.hkv + wk.g) * a.kv.max_seq_len;
-      int page[4], y[4];
-      uint32_t bad = 0, any_bad = 0;
-      auto fetch = [&](int tile) {   // asks for the page numbers of this lane's rows of 32 boxes
-        const int t = tile * TT + lane * per;
-        page[0] = paged && t < len ? __ldg(table + (t >> shift)) : 0;
-        if (gather) {
-#pragma unroll
-          for (int e = 1; e < 4; ++e) page[e] = t + e < len ? __ldg(table + ((t + e) >> shift)) : 0;
-        }
-      };
-      auto resolve = [&](int tile) {
-        const int t = tile * TT + lane * per;
-        if (!paged) {
-          y[0] = head_row + t;
-        } else {
-          bad = (uint32_t)page[0] >= num_pages;
-          y[0] = bad ? no_row : page[0] * page_rows + head_row + (t & in_page);
-          if (gather) {
-#pragma unroll
-            for (int e = 1; e < 4; ++e) {
-              const bool none = (uint32_t)page[e] >= num_pages;
-              bad |= (uint32_t)none << e;
-              y[e] = none ? no_row : page[e] * page_rows + head_row + ((t + e) & in_page);
-            }
-          }
-          any_bad = __ballot_sync(0xFFFFFFFFu, bad != 0);
-          if (bad && !is_v) flag_optional(a.status, TSD_DEV_BAD_PAGE);
-        }
-      };
-      fetch(wk.k0);
-#pragma unroll 1
-      for (int tile = wk.k0, w = 0; tile < wk.k1; ++tile, ++n) {
-        if (w == 0) {
-          resolve(tile);
-          if (tile + window < wk.k1) fetch(tile + window);
-        }
-        const int box0 = w * per_tile, boxes = min(per_tile, (len - tile * TT + per - 1) / per);
-        if (++w == window) w = 0;
-        if (round > 0) tree_wait_warp(&empty[slot], (round - 1) & 1, ctl, a.status);
-        if (!is_v) {
-          uint32_t* marks = ctl->bad[n & 31];
-          if (lane < 2) marks[lane] = 0;
-          if (any_bad >> box0 & low_bits(per_tile)) {   // rows of bad pages, as bits of the tile
-            __syncwarp();
-            const int r0 = (lane - box0) * per;
-            if (lane >= box0 && r0 < TT)
-#pragma unroll 1
-              for (int e = 0; e < per; ++e)
-                if (bad & (gather ? 1u << e : 1u)) atomicOr(&marks[(r0 + e) >> 5], 1u << ((r0 + e) & 31));
-          }
-          __syncwarp();
-        }
-        unsigned char* dst = ring + slot * SH::kSlotBytes;
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(boxes * per * 256));
-        // one thread issues: a TMA instruction with other operands in every lane is split up
-        if (gather) {
-#pragma unroll 1
-          for (int i = 0; i < boxes; ++i) {
-            int yi[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) yi[e] = __shfl_sync(0xFFFFFFFFu, y[e], box0 + i);
-            if (lane == 0) {
-              tma_gather4_hint(dst + i * 512, map, 0, yi, &full[slot], pol);
-              tma_gather4_hint(dst + TT * 128 + i * 512, map, 64, yi, &full[slot], pol);
-            }
-          }
-        } else {
-#pragma unroll 1
-          for (int i = 0; i < boxes; ++i) {
-            const int yi = __shfl_sync(0xFFFFFFFFu, y[0], box0 + i);
-            if (lane == 0) {
-              tma_load_2d_hint(dst + i * per * 128, map, 0, yi, &full[slot], pol);
-              tma_load_2d_hint(dst + TT * 128 + i * per * 128, map, 64, yi, &full[slot], pol);
-            }
-          }
-        }
-        if (++slot == slots) {
-          slot = 0;
-          ++round;
-        }
-      }
-    }
-    // no copy may be in flight when the CTA ends: the fills of this round, then of the one before
-#pragma unroll 1
-    for (uint32_t i = 0; i < slot; ++i) tree_wait_warp(&full[i], round & 1, ctl, a.status);
-    if (round > 0)
-#pragma unroll 1
-      for (uint32_t i = slot; i < slots; ++i) tree_wait_warp(&full[i], (round - 1) & 1, ctl, a.status);
-  }
-  else if (warp == 8 || warp == 9) {
-    // ---- MMA issuers: one thread for each stream.  A step's products are followed by the scores of the
-    // step after next, into the buffer that the products have just read (MMAs run in order).
-    if (lane == 0) {
-      const int s = warp - 8;
-      constexpr uint32_t idesc_s = umma_idesc_bf16_f32(128, TT), idesc_o = umma_idesc_bf16_f32_bmn(128, 128);
-      const uint64_t q_desc = sw128_desc(smem_u32(qtile), 1024), ring_k = sw128_desc(smem_u32(kring), 1024),
-                     ring_v = sw128_mn_desc(smem_u32(vring), TT * 128, 1024);
-      const uint32_t tm = tmem + s * 256;
-      uint32_t tiles_done = 0, done = 0, fixes = 0, segs = 0;
-#pragma unroll 1
-      for (; wk.live(); wk.next(a, G), ++segs) {
-        const bool dual = wk.dual(G);
-        const int ntile = wk.k1 - wk.k0, stride = dual ? 1 : 2, first = dual ? 0 : s;
-        const int steps = (ntile - first + stride - 1) / stride;
-        const uint64_t qd = q_desc + (dual && s ? 32768 >> 4 : 0);
-        tree_wait(&ctl->q_ready, segs & 1, ctl, a.status);
-        tc_fence_after_sync();
-        auto scores = [&](int i) {
-          const uint32_t n = tiles_done + first + stride * i, slot = n % KS, buf = (done + i) & 1;
-          tree_wait(&ctl->k_full[slot], (n / KS) & 1, ctl, a.status);
-          tc_fence_after_sync();
-          const uint64_t kd = ring_k + (uint64_t)(slot * (SH::kSlotBytes >> 4));
-#pragma unroll
-          for (int p = QP - 1; p >= 0; --p)   // the small parts first: every step rounds the sum so far
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              umma_bf16(tm + buf * 64, qd + ((p * 32768 + (ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
-                        kd + (((ks >> 2) * (TT * 128) + (ks & 3) * 32) >> 4), idesc_s, p < QP - 1 || ks > 0);
-          umma_commit(&ctl->s_full[s][buf]);
-          umma_commit(&ctl->k_empty[slot]);   // expects both streams; a tile of one stream counts twice
-          if (!dual) umma_commit(&ctl->k_empty[slot]);
-        };
-#pragma unroll 1
-        for (int i = -2; i < steps; ++i) {
-          const int at = first + stride * i;
-          if (i >= 0) {
-            const uint32_t n = tiles_done + at, slot = n % VS, buf = (done + i) & 1;
-            tree_wait(&ctl->v_full[slot], (n / VS) & 1, ctl, a.status);
-            tree_wait(&ctl->p_ready[s][buf], ((done + i) >> 1) & 1, ctl, a.status);
-            tc_fence_after_sync();
-            const uint64_t vd = ring_v + (uint64_t)(slot * (SH::kSlotBytes >> 4));
-            const bool fresh = SH::kFlush ? i % (SH::kFlush ? SH::kFlush : 1) == 0 : i == 0;
-#pragma unroll
-            for (int p = PP - 1; p >= 0; --p)
-#pragma unroll
-              for (int ks = 0; ks < TT / 16; ++ks)
-                umma_bf16_ts(tm + 128, tm + buf * 64 + p * (TT / 2) + ks * 8, vd + (ks * 2048 >> 4), idesc_o,
-                             !fresh || p < PP - 1 || ks > 0);
-            umma_commit(&ctl->o_done[s][buf]);
-            umma_commit(&ctl->v_empty[slot]);
-            if (!dual) umma_commit(&ctl->v_empty[slot]);
-          }
-          if (i + 2 < steps) {
-            if (i >= 0 && (wk.k0 + at + 1) * TT > wk.s.base) {   // a special tile: P is read once more
-              tree_wait(&ctl->fixed[s], fixes++ & 1, ctl, a.status);
-              tc_fence_after_sync();
-            }
-            scores(i + 2);
-          }
-        }
-        tiles_done += ntile;
-        done += steps;
-      }
-      // no MMA may be in flight when tensor memory is freed
-      umma_commit(&ctl->drain[s]);
-      if (!mbar_wait(&ctl->drain[s], 0)) flag_optional(a.status, TSD_DEV_TIMEOUT);
-    }
-    __syncwarp();
-  } else if (warp < 8) {
+  if (warp < 8) {
+    take_registers<kTaSoftmaxRegs>();
+    TreeWalk<SH> wk;
+    wk.start(a, G, ctl->b0, ctl->off, share);
     // ---- softmax: a list a thread
     const int s = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;   // this warp's tensor-memory lanes
@@ -978,6 +805,190 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       }
       tc_fence_before_sync();
     }
+  } else {
+    give_registers<kTaOtherRegs>();
+    TreeWalk<SH> wk;
+    wk.start(a, G, ctl->b0, ctl->off, share);
+  if (warp >= 10 && warp < 14) {
+    // ---- producers: warp 10 loads K, warp 11 V, tile n of the share into slot n % slots of its ring.
+    // The TMA unit takes about 80 cycles for a box of 16 rows x 128 bytes, 25 bytes a cycle against
+    // the 23 that are an SM's part of the HBM rate, so little may stand between the boxes: the page
+    // numbers of 32 boxes are fetched and resolved at once, the next 32 while those are used.
+    const bool is_v = warp & 1;
+    const uint32_t odd = (warp - 10) >> 1;
+    const CUtensorMap* map = is_v ? &maps.v : &maps.k;
+    unsigned char* ring = is_v ? vring : kring;
+    uint64_t *full = is_v ? ctl->v_full : ctl->k_full, *empty = is_v ? ctl->v_empty : ctl->k_empty;
+    const uint32_t slots = is_v ? VS : KS;
+    // Pages of 8 or more tokens: boxes of `per` rows, one a lane; smaller pages: four rows a lane.
+    const bool paged = a.kv.page_table != nullptr, gather = paged && a.kv.page_shift < 3;
+    const int shift = paged ? a.kv.page_shift : 0, in_page = (1 << shift) - 1;
+    const int per = !paged ? TT : (gather ? 4 : min(TT, 1 << shift));
+    const int per_tile = TT / per, window = 32 / per_tile;   // boxes of a tile, tiles of 32 boxes
+    const int page_rows = a.kv.hkv << shift, no_row = (int)(a.kv.num_pages * page_rows);   // no_row: zeros arrive
+    const uint32_t num_pages = (uint32_t)a.kv.num_pages;
+    uint32_t n = 0;
+#pragma unroll 1
+    for (; wk.live(); wk.next(a, G)) {
+      const int len = wk.s.len;
+      // rows that no other unit reads are the first to leave L2
+      const uint64_t pol = wk.s.mtiles == 1 ? l2_evict_first() : l2_evict_normal();
+      const int32_t* table = a.kv.page_table + (int64_t)wk.b * a.kv.max_pages;
+      const int head_row = paged ? wk.g << shift : (wk.b * a.kv.hkv + wk.g) * a.kv.max_seq_len;
+      int page[4], y[4];
+      uint32_t bad = 0, any_bad = 0;
+      auto fetch = [&](int tile) {   // asks for the page numbers of this lane's rows of 32 boxes
+        const int t = tile * TT + lane * per;
+        page[0] = paged && t < len ? __ldg(table + (t >> shift)) : 0;
+        if (gather) {
+#pragma unroll
+          for (int e = 1; e < 4; ++e) page[e] = t + e < len ? __ldg(table + ((t + e) >> shift)) : 0;
+        }
+      };
+      auto resolve = [&](int tile) {
+        const int t = tile * TT + lane * per;
+        if (!paged) {
+          y[0] = head_row + t;
+        } else {
+          bad = (uint32_t)page[0] >= num_pages;
+          y[0] = bad ? no_row : page[0] * page_rows + head_row + (t & in_page);
+          if (gather) {
+#pragma unroll
+            for (int e = 1; e < 4; ++e) {
+              const bool none = (uint32_t)page[e] >= num_pages;
+              bad |= (uint32_t)none << e;
+              y[e] = none ? no_row : page[e] * page_rows + head_row + ((t + e) & in_page);
+            }
+          }
+          any_bad = __ballot_sync(0xFFFFFFFFu, bad != 0);
+          if (bad && !is_v) flag_optional(a.status, TSD_DEV_BAD_PAGE);
+        }
+      };
+      fetch(wk.k0);
+#pragma unroll 1
+      for (int tile = wk.k0, w = 0; tile < wk.k1; ++tile, ++n) {
+        if (w == 0) {
+          resolve(tile);
+          if (tile + window < wk.k1) fetch(tile + window);
+        }
+        const uint32_t slot = n % slots, round = n / slots;
+        const int box0 = w * per_tile, boxes = min(per_tile, (len - tile * TT + per - 1) / per);
+        if (++w == window) w = 0;
+        if ((n & 1) != odd) continue;
+        if (round > 0) tree_wait_warp(&empty[slot], (round - 1) & 1, ctl, a.status);
+        if (!is_v) {
+          uint32_t* marks = ctl->bad[n & 31];
+          if (lane < 2) marks[lane] = 0;
+          if (any_bad >> box0 & low_bits(per_tile)) {   // rows of bad pages, as bits of the tile
+            __syncwarp();
+            const int r0 = (lane - box0) * per;
+            if (lane >= box0 && r0 < TT)
+#pragma unroll 1
+              for (int e = 0; e < per; ++e)
+                if (bad & (gather ? 1u << e : 1u)) atomicOr(&marks[(r0 + e) >> 5], 1u << ((r0 + e) & 31));
+          }
+          __syncwarp();
+        }
+        unsigned char* dst = ring + slot * SH::kSlotBytes;
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(boxes * per * 256));
+        // one thread issues: a TMA instruction with other operands in every lane is split up
+        if (gather) {
+#pragma unroll 1
+          for (int i = 0; i < boxes; ++i) {
+            int yi[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) yi[e] = __shfl_sync(0xFFFFFFFFu, y[e], box0 + i);
+            if (lane == 0) {
+              tma_gather4_hint(dst + i * 512, map, 0, yi, &full[slot], pol);
+              tma_gather4_hint(dst + TT * 128 + i * 512, map, 64, yi, &full[slot], pol);
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < boxes; ++i) {
+            const int yi = __shfl_sync(0xFFFFFFFFu, y[0], box0 + i);
+            if (lane == 0) {
+              tma_load_2d_hint(dst + i * per * 128, map, 0, yi, &full[slot], pol);
+              tma_load_2d_hint(dst + TT * 128 + i * per * 128, map, 64, yi, &full[slot], pol);
+            }
+          }
+        }
+      }
+    }
+    // no copy may be in flight when the CTA ends
+#pragma unroll 1
+    for (uint32_t i = n > slots ? n - slots : 0; i < n; ++i) tree_wait_warp(&full[i % slots], (i / slots) & 1, ctl, a.status);
+  }
+  else if (warp == 8 || warp == 9) {
+    // ---- MMA issuers: one thread for each stream.  A step's products are followed by the scores of the
+    // step after next, into the buffer that the products have just read (MMAs run in order).
+    if (lane == 0) {
+      const int s = warp - 8;
+      constexpr uint32_t idesc_s = umma_idesc_bf16_f32(128, TT), idesc_o = umma_idesc_bf16_f32_bmn(128, 128);
+      const uint64_t q_desc = sw128_desc(smem_u32(qtile), 1024), ring_k = sw128_desc(smem_u32(kring), 1024),
+                     ring_v = sw128_mn_desc(smem_u32(vring), TT * 128, 1024);
+      const uint32_t tm = tmem + s * 256;
+      uint32_t tiles_done = 0, done = 0, fixes = 0, segs = 0;
+#pragma unroll 1
+      for (; wk.live(); wk.next(a, G), ++segs) {
+        const bool dual = wk.dual(G);
+        const int ntile = wk.k1 - wk.k0, stride = dual ? 1 : 2, first = dual ? 0 : s;
+        const int steps = (ntile - first + stride - 1) / stride;
+        const uint64_t qd = q_desc + (dual && s ? 32768 >> 4 : 0);
+        tree_wait(&ctl->q_ready, segs & 1, ctl, a.status);
+        tc_fence_after_sync();
+        auto scores = [&](int i) {
+          const uint32_t n = tiles_done + first + stride * i, slot = n % KS, buf = (done + i) & 1;
+          tree_wait(&ctl->k_full[slot], (n / KS) & 1, ctl, a.status);
+          tc_fence_after_sync();
+          const uint64_t kd = ring_k + (uint64_t)(slot * (SH::kSlotBytes >> 4));
+#pragma unroll
+          for (int p = QP - 1; p >= 0; --p)   // the small parts first: every step rounds the sum so far
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              umma_bf16(tm + buf * 64, qd + ((p * 32768 + (ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
+                        kd + (((ks >> 2) * (TT * 128) + (ks & 3) * 32) >> 4), idesc_s, p < QP - 1 || ks > 0);
+          umma_commit(&ctl->s_full[s][buf]);
+          umma_commit(&ctl->k_empty[slot]);   // expects both streams; a tile of one stream counts twice
+          if (!dual) umma_commit(&ctl->k_empty[slot]);
+        };
+#pragma unroll 1
+        for (int i = -2; i < steps; ++i) {
+          const int at = first + stride * i;
+          if (i >= 0) {
+            const uint32_t n = tiles_done + at, slot = n % VS, buf = (done + i) & 1;
+            tree_wait(&ctl->v_full[slot], (n / VS) & 1, ctl, a.status);
+            tree_wait(&ctl->p_ready[s][buf], ((done + i) >> 1) & 1, ctl, a.status);
+            tc_fence_after_sync();
+            const uint64_t vd = ring_v + (uint64_t)(slot * (SH::kSlotBytes >> 4));
+            const bool fresh = SH::kFlush ? i % (SH::kFlush ? SH::kFlush : 1) == 0 : i == 0;
+#pragma unroll
+            for (int p = PP - 1; p >= 0; --p)
+#pragma unroll
+              for (int ks = 0; ks < TT / 16; ++ks)
+                umma_bf16_ts(tm + 128, tm + buf * 64 + p * (TT / 2) + ks * 8, vd + (ks * 2048 >> 4), idesc_o,
+                             !fresh || p < PP - 1 || ks > 0);
+            umma_commit(&ctl->o_done[s][buf]);
+            umma_commit(&ctl->v_empty[slot]);
+            if (!dual) umma_commit(&ctl->v_empty[slot]);
+          }
+          if (i + 2 < steps) {
+            if (i >= 0 && (wk.k0 + at + 1) * TT > wk.s.base) {   // a special tile: P is read once more
+              tree_wait(&ctl->fixed[s], fixes++ & 1, ctl, a.status);
+              tc_fence_after_sync();
+            }
+            scores(i + 2);
+          }
+        }
+        tiles_done += ntile;
+        done += steps;
+      }
+      // no MMA may be in flight when tensor memory is freed
+      umma_commit(&ctl->drain[s]);
+      if (!mbar_wait(&ctl->drain[s], 0)) flag_optional(a.status, TSD_DEV_TIMEOUT);
+    }
+    __syncwarp();
+  }
   }
   __syncthreads();
   if (warp == 10) {
