@@ -198,6 +198,9 @@ struct TreeShares {
   }
 };
 
+// CTAs that share `total` tiles: two tiles each at least, one a stream.
+__host__ __device__ __forceinline__ int tree_ctas(int ctas, int total) { return min(ctas, (total + 1) / 2); }
+
 // The segments of a CTA's share, in order; every warp role walks them by itself.
 template <class SH>
 struct TreeWalk {
@@ -282,6 +285,13 @@ __device__ __forceinline__ void take_registers() {
 template <int N>
 __device__ __forceinline__ void give_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
 }
 
 __device__ __forceinline__ void named_sync(int id, int threads) {
@@ -478,7 +488,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   unsigned char* kring = ta_smem + SH::kQBytes;
   unsigned char* vring = kring + KS * SH::kSlotBytes;
   TreeCtl* ctl = reinterpret_cast<TreeCtl*>(ta_smem + kTaTiles);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the broadcast tells the compiler that the role, and what follows from it, is the same for a warp
+  const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   const int G = a.qv.hq / a.kv.hkv;
   pdl_launch_dependents();
   if (smem_u32(ta_smem) & 1023u) {   // the swizzled tiles need 1024-byte alignment
@@ -549,7 +560,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     }
     if (pass == 0) {
       total = run;
-      const int C = min(a.ctas, total);
+      const int C = tree_ctas(a.ctas, total);
       if ((int)blockIdx.x < C) {
         const TreeShares shares(total, C);
         begin = shares.begin(blockIdx.x);
@@ -890,7 +901,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           __syncwarp();
         }
         unsigned char* dst = ring + slot * SH::kSlotBytes;
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(boxes * per * 256));
+        const bool one = elect_one();
+        if (one) mbar_arrive_expect_tx(&full[slot], (uint32_t)(boxes * per * 256));
         // one thread issues: a TMA instruction with other operands in every lane is split up
         if (gather) {
 #pragma unroll 1
@@ -898,7 +910,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             int yi[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) yi[e] = __shfl_sync(0xFFFFFFFFu, y[e], box0 + i);
-            if (lane == 0) {
+            if (one) {
               tma_gather4_hint(dst + i * 512, map, 0, yi, &full[slot], pol);
               tma_gather4_hint(dst + TT * 128 + i * 512, map, 64, yi, &full[slot], pol);
             }
@@ -907,7 +919,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 #pragma unroll 1
           for (int i = 0; i < boxes; ++i) {
             const int yi = __shfl_sync(0xFFFFFFFFu, y[0], box0 + i);
-            if (lane == 0) {
+            if (one) {
               tma_load_2d_hint(dst + i * per * 128, map, 0, yi, &full[slot], pol);
               tma_load_2d_hint(dst + TT * 128 + i * per * 128, map, 64, yi, &full[slot], pol);
             }
@@ -922,7 +934,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   else if (warp == 8 || warp == 9) {
     // ---- MMA issuers: one thread for each stream.  A step's products are followed by the scores of the
     // step after next, into the buffer that the products have just read (MMAs run in order).
-    if (lane == 0) {
+    {
       const int s = warp - 8;
       constexpr uint32_t idesc_s = umma_idesc_bf16_f32(128, TT), idesc_o = umma_idesc_bf16_f32_bmn(128, 128);
       const uint64_t q_desc = sw128_desc(smem_u32(qtile), 1024), ring_k = sw128_desc(smem_u32(kring), 1024),
@@ -935,12 +947,13 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         const int ntile = wk.k1 - wk.k0, stride = dual ? 1 : 2, first = dual ? 0 : s;
         const int steps = (ntile - first + stride - 1) / stride;
         const uint64_t qd = q_desc + (dual && s ? 32768 >> 4 : 0);
-        tree_wait(&ctl->q_ready, segs & 1, ctl, a.status);
+        tree_wait_warp(&ctl->q_ready, segs & 1, ctl, a.status);
         tc_fence_after_sync();
         auto scores = [&](int i) {
           const uint32_t n = tiles_done + first + stride * i, slot = n % KS, buf = (done + i) & 1;
-          tree_wait(&ctl->k_full[slot], (n / KS) & 1, ctl, a.status);
+          tree_wait_warp(&ctl->k_full[slot], (n / KS) & 1, ctl, a.status);
           tc_fence_after_sync();
+          if (!elect_one()) return;
           const uint64_t kd = ring_k + (uint64_t)(slot * (SH::kSlotBytes >> 4));
 #pragma unroll
           for (int p = QP - 1; p >= 0; --p)   // the small parts first: every step rounds the sum so far
@@ -957,9 +970,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           const int at = first + stride * i;
           if (i >= 0) {
             const uint32_t n = tiles_done + at, slot = n % VS, buf = (done + i) & 1;
-            tree_wait(&ctl->v_full[slot], (n / VS) & 1, ctl, a.status);
-            tree_wait(&ctl->p_ready[s][buf], ((done + i) >> 1) & 1, ctl, a.status);
+            tree_wait_warp(&ctl->v_full[slot], (n / VS) & 1, ctl, a.status);
+            tree_wait_warp(&ctl->p_ready[s][buf], ((done + i) >> 1) & 1, ctl, a.status);
             tc_fence_after_sync();
+            if (elect_one()) {
             const uint64_t vd = ring_v + (uint64_t)(slot * (SH::kSlotBytes >> 4));
             const bool fresh = SH::kFlush ? i % (SH::kFlush ? SH::kFlush : 1) == 0 : i == 0;
 #pragma unroll
@@ -971,21 +985,26 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             umma_commit(&ctl->o_done[s][buf]);
             umma_commit(&ctl->v_empty[slot]);
             if (!dual) umma_commit(&ctl->v_empty[slot]);
+            }
+            __syncwarp();
           }
           if (i + 2 < steps) {
             if (i >= 0 && (wk.k0 + at + 1) * TT > wk.s.base) {   // a special tile: P is read once more
-              tree_wait(&ctl->fixed[s], fixes++ & 1, ctl, a.status);
+              tree_wait_warp(&ctl->fixed[s], fixes++ & 1, ctl, a.status);
               tc_fence_after_sync();
             }
             scores(i + 2);
+            __syncwarp();
           }
         }
         tiles_done += ntile;
         done += steps;
       }
       // no MMA may be in flight when tensor memory is freed
-      umma_commit(&ctl->drain[s]);
-      if (!mbar_wait(&ctl->drain[s], 0)) flag_optional(a.status, TSD_DEV_TIMEOUT);
+      if (elect_one()) {
+        umma_commit(&ctl->drain[s]);
+        if (!mbar_wait(&ctl->drain[s], 0)) flag_optional(a.status, TSD_DEV_TIMEOUT);
+      }
     }
     __syncwarp();
   }
@@ -998,14 +1017,23 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 }
 
 // Merge of the partial states of units cut over several CTAs, in the order of the shares.  One block
-// per 32 lists of a (sequence, kv head); a lane per list, so that the states' rows are read whole,
-// and four dims of it at a time.
+// per 32 lists of a (sequence, kv head) and kTgDims of their dims; a lane per list, so that the
+// states' rows are read whole.  The warps first find the shares' weights, which stay in shared memory,
+// then take four dims each, in two halves of the shares: few lists with many shares (one short step of
+// one user: 65 shares) need many loads under way.
 constexpr int kTgThreads = 256;
+constexpr int kTgDims = 16;
+constexpr int kTgWarps = kTgThreads / 32;
 
 template <int QP, int PP>
 __global__ void __launch_bounds__(kTgThreads) tree_merge_kernel(const __grid_constant__ TreeArgs a, int groups) {
   using SH = TreeShape<QP, PP>;
-  const int rg = blockIdx.x % groups, g = (blockIdx.x / groups) % a.kv.hkv, b = blockIdx.x / groups / a.kv.hkv;
+  extern __shared__ float tg_w[];   // [shares of the unit][32]
+  __shared__ float red[kTgWarps][32];
+  __shared__ float4 half[4][32];
+  constexpr int kSlices = kHeadDim / kTgDims;
+  const int slice = blockIdx.x % kSlices, unit = blockIdx.x / kSlices;
+  const int rg = unit % groups, g = (unit / groups) % a.kv.hkv, b = unit / groups / a.kv.hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.qv.hq / a.kv.hkv;
   const TreeSeq sq = tree_seq<SH>(a, b, G, false);
@@ -1013,50 +1041,65 @@ __global__ void __launch_bounds__(kTgThreads) tree_merge_kernel(const __grid_con
   pdl_wait();
   if (rg * 32 >= lists) return;
   const int total = a.line[0];
-  const TreeShares shares(total, min(a.ctas, total));
+  const TreeShares shares(total, tree_ctas(a.ctas, total));
   const int mt = rg * 32 / SH::kRows, u0 = a.line[1 + b] + (g * sq.mtiles + mt) * sq.tiles;
-  const int c0 = shares.owner(u0), c1 = shares.owner(u0 + sq.tiles - 1);
-  if (c0 == c1) return;   // written directly
+  const int c0 = shares.owner(u0), parts = shares.owner(u0 + sq.tiles - 1) - c0 + 1;
+  if (parts == 1) return;   // written directly
   const int list = rg * 32 + lane, prow = list - mt * SH::kRows;
-  if (list >= lists) return;
-  auto slot = [&](int c) { return 2 * (int64_t)c + (c == c0 ? 1 : 0); };
+  const bool valid = list < lists;
+  const int row = min(prow, a.part_rows - 1);
   // the first share of the unit starts at its first tile: its state is in the odd slot
+  auto slot = [&](int p) { return 2 * (int64_t)(c0 + p) + (p == 0 ? 1 : 0); };
   float m = -INFINITY;
-  for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(&a.part_ml[slot(c) * a.part_rows + prow].x));
-  float l = 0.f, o[4][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 #pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const int64_t sl = slot(c);
-    const float2 ml = __ldcg(a.part_ml + sl * a.part_rows + prow);
-    const float w = ml.x == m ? 1.f : fast_exp2(ml.x - m);
-    if (ml.x == -INFINITY) continue;   // nothing seen in this share
-    l += w * ml.y;
+  for (int p = warp; p < parts; p += kTgWarps) {
+    const float x = valid ? __ldcg(&a.part_ml[slot(p) * a.part_rows + row].x) : -INFINITY;
+    tg_w[p * 32 + lane] = x;
+    m = fmaxf(m, x);
+  }
+  red[warp][lane] = m;
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 x = __ldcg(a.part_acc + (sl * 32 + warp + 8 * i) * a.part_rows + prow);
-      o[i][0] += w * x.x;
-      o[i][1] += w * x.y;
-      o[i][2] += w * x.z;
-      o[i][3] += w * x.w;
+  for (int w = 0; w < kTgWarps; ++w) m = fmaxf(m, red[w][lane]);
+  __syncthreads();
+  float l = 0.f;
+#pragma unroll 4
+  for (int p = warp; p < parts; p += kTgWarps) {
+    const float x = tg_w[p * 32 + lane];
+    const float w = x == -INFINITY ? 0.f : (x == m ? 1.f : fast_exp2(x - m));
+    tg_w[p * 32 + lane] = w;
+    if (x != -INFINITY) l += w * __ldcg(&a.part_ml[slot(p) * a.part_rows + row].y);
+  }
+  red[warp][lane] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kTgWarps; ++w) l += red[w][lane];
+  const int d4 = slice * (kTgDims / 4) + (warp & 3);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int p = warp >> 2; p < parts; p += 2) {
+    const float w = tg_w[p * 32 + lane];
+    const float4 x = __ldcg(a.part_acc + (slot(p) * 32 + d4) * a.part_rows + row);
+    if (w != 0.f) {   // a share in which the list saw nothing holds no numbers
+      o.x += w * x.x;
+      o.y += w * x.y;
+      o.z += w * x.z;
+      o.w += w * x.w;
     }
   }
-  const int j = list / G;
-  const int64_t lst = (int64_t)(sq.t0 + j) * a.qv.hq + g * G + (list - j * G);
+  if (warp >= 4) half[warp - 4][lane] = o;
+  __syncthreads();
+  if (warp >= 4 || !valid) return;
+  const float4 y = half[warp][lane];
   const float norm = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t at = lst * 32 + warp + 8 * i;
-    if (a.out_f32)
-      static_cast<float4*>(a.out)[at] = make_float4(o[i][0] * norm, o[i][1] * norm, o[i][2] * norm, o[i][3] * norm);
-    else
-      static_cast<uint2*>(a.out)[at] =
-          make_uint2(cvt_bf16x2(o[i][0] * norm, o[i][1] * norm), cvt_bf16x2(o[i][2] * norm, o[i][3] * norm));
-  }
-  if (warp == 0 && a.lse != nullptr) a.lse[lst] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+  o = make_float4((o.x + y.x) * norm, (o.y + y.y) * norm, (o.z + y.z) * norm, (o.w + y.w) * norm);
+  const int j = list / G;
+  const int64_t lst = (int64_t)(sq.t0 + j) * a.qv.hq + g * G + (list - j * G), at = lst * 32 + d4;
+  if (a.out_f32) static_cast<float4*>(a.out)[at] = o;
+  else static_cast<uint2*>(a.out)[at] = make_uint2(cvt_bf16x2(o.x, o.y), cvt_bf16x2(o.z, o.w));
+  if (warp == 0 && slice == 0 && a.lse != nullptr)
+    a.lse[lst] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
 struct TreeLayout {
@@ -1083,8 +1126,8 @@ static cudaError_t launch_tree(const TreeArgs& a, const KvMaps& maps, int64_t ba
   tree_decode_kernel<QP, PP><<<a.ctas, kTaThreads, kTaSmem, stream>>>(a, maps);
   const cudaError_t e2 = cudaGetLastError();
   if (e2 != cudaSuccess) return e2;
-  return launch_dependent(tree_merge_kernel<QP, PP>, dim3((unsigned)(batch * a.kv.hkv * groups)), dim3(kTgThreads), 0,
-                          stream, a, groups);
+  return launch_dependent(tree_merge_kernel<QP, PP>, dim3((unsigned)(batch * a.kv.hkv * groups * (kHeadDim / kTgDims))),
+                          dim3(kTgThreads), (size_t)a.ctas * 32 * sizeof(float), stream, a, groups);
 }
 
 }  // namespace tsd
@@ -1145,7 +1188,7 @@ tsd_status tsd_tree_decode(const tsd_kv_cache* cache, const tsd_queries* queries
   if (ws_bytes < l.total) return TSD_ERR_WORKSPACE_TOO_SMALL;
   const int64_t groups = (sh.group * sh.max_tokens + 31) / 32;
   // the line of tiles and the merge's grid are counted in 32 bits
-  if ((double)sh.batch * sh.hkv * groups * ((double)sh.max_seq_len / 32 + 1) >= 2147483647.0) return TSD_ERR_UNSUPPORTED;
+  if ((double)sh.batch * sh.hkv * groups * ((double)sh.max_seq_len / 32 + 8) >= 2147483647.0) return TSD_ERR_UNSUPPORTED;
   a.mask = mask;
   a.words = (int)(sh.max_tokens + 31) / 32;
   a.part_rows = l.part_rows;
