@@ -298,6 +298,8 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
   __syncwarp();
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }
+__device__ __forceinline__ void pair_wait(int id) { asm volatile("bar.sync %0, 64;\n" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void pair_arrive(int id) { asm volatile("bar.arrive %0, 64;\n" ::"r"(id) : "memory"); }
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
@@ -594,6 +596,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       const int first = wk.mt * SH::kRows + (dual ? s * kTaRowsPerStream : 0);
       const int list = first + row;
       const bool valid = list < lists, warp_live = first + 32 * (warp & 3) < lists;
+      // the warp of the other stream on the same quarter of the SM has work too
+      const bool pair = dual && wk.mt * SH::kRows + kTaRowsPerStream + 32 * (warp & 3) < lists;
+      if (pair && s == 1) pair_arrive(4 + 2 * (warp & 3));   // stream 0 goes first
       const int j = list / G, h = wk.g * G + (list - j * G);
       named_sync(1, 256);   // the previous segment's Q tiles and states are done with
       {
@@ -686,6 +691,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;   // nothing seen yet: weights 0
+          if (pair) pair_wait(4 + 2 * (warp & 3) + s);
           const float2 scale2 = make_float2(scale, scale), ref2 = make_float2(-ref, -ref);
           float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -712,6 +718,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
               tmem_st16(tp + part * (TT / 2) + 16 * c, w);
             }
           }
+          if (pair) pair_arrive(4 + 2 * (warp & 3) + (s ^ 1));
           l2[0] = __fadd2_rn(l2[0], l2[1]);
           l += l2[0].x + l2[0].y;
           tmem_wait_st();
@@ -735,6 +742,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           if (i + 2 < steps) mbar_arrive(&ctl->fixed[s]);
         }
       }
+      if (pair && s == 0) pair_wait(4 + 2 * (warp & 3));   // the other stream's last turn
       if (steps > 0) {
         const uint32_t last = done + steps - 1;
         tree_wait_warp(&ctl->o_done[s][last & 1], (last >> 1) & 1, ctl, a.status);
