@@ -287,6 +287,16 @@ __device__ __forceinline__ void give_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
+// Whether the phase of the given parity is complete.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
@@ -656,27 +666,30 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           tree_flush(to, sums, m_sum == -INFINITY ? 0.f : fast_exp2(m_sum - m), m_sum != -INFINITY, valid);
           m_sum = m;
         }
-        tree_wait_warp(&ctl->s_full[s][step & 1], (step >> 1) & 1, ctl, a.status);
+        if (!__all_sync(0xFFFFFFFFu, mbar_test(&ctl->s_full[s][step & 1], (step >> 1) & 1)))
+          tree_wait_warp(&ctl->s_full[s][step & 1], (step >> 1) & 1, ctl, a.status);
         tc_fence_after_sync();
         if (warp_live) {
           float x[TT];
 #pragma unroll
           for (int c = 0; c < TT / 32; ++c) tmem_ld32(tp + 32 * c, x + 32 * c);
+          const volatile uint32_t* marks = ctl->bad[num & 31];
+          const uint32_t bad0 = marks[0], bad1 = TT > 32 ? marks[1] : 0;
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < TT / 32; ++c) tmem_loaded32(x + 32 * c);
-          const volatile uint32_t* marks = ctl->bad[num & 31];
-          uint64_t bad = marks[0];
-          if (TT > 32) bad |= (uint64_t)marks[1] << 32;
-          if (special || bad != 0) {
+          if (special || (bad0 | bad1)) {
+            const uint64_t bad = (uint64_t)bad1 << 32 | bad0;
             seen = valid ? tree_visible<TT>(a, sq, j, tile * TT) & ~bad : 0u;
 #pragma unroll
             for (int c = 0; c < TT; ++c) x[c] = seen >> c & 1 ? x[c] : -INFINITY;
           }
-          float mx4[4] = {x[0], x[1], x[2], x[3]};
+          float mx8[8];
 #pragma unroll
-          for (int c = 4; c + 1 < TT; c += 2) mx4[(c >> 1) & 3] = max3(mx4[(c >> 1) & 3], x[c], x[c + 1]);
-          const float mx = max3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3])) * scale;
+          for (int c = 0; c < 8; ++c) mx8[c] = x[c];
+#pragma unroll
+          for (int c = 8; c < TT; c += 2) mx8[(c >> 1) & 7] = max3(mx8[(c >> 1) & 7], x[c], x[c + 1]);
+          const float mx = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])) * scale;
           if (i == 0) {
             m = mx;
           } else {
