@@ -25,41 +25,61 @@ from __future__ import annotations
 import ctypes
 from typing import Optional
 
-from . import (DEV_BAD_SEQ, TSD_BF16, TSD_ERR_INVALID_ARGUMENT, TSD_F32, KVCache, Queries, TsdError, Workspace,  # noqa: F401
-               _check, _KvCacheC, _LayerC, _QueriesC, _RopeC, _RopeScalingC, _shape_key, load_library)
+from . import (TSD_BF16, TSD_ERR_INVALID_ARGUMENT, TSD_F32, KVCache, Queries, TsdError, Workspace, _check, _LayerC,
+               _QueriesC, _RopeC, _RopeScalingC, load_library)
 
 _SCALING = {"linear": 1, "ntk": 2, "banded": 3, "yarn": 4}
 
 _STATUS = {}   # device index -> the status word of calls without one of their own
 
+# A step of one layer is a handful of calls, each a few microseconds on the GPU for a small batch, so what the
+# calls do on the host is kept short: torch and the library are looked up once, and the device and stream are
+# made current only where they are not.
+torch = None
+_LIB = None
 
-class _Call:
-    """The device and stream of one call: `with` makes them current where they are not already."""
+
+def _ready():
+    global torch, _LIB
+    if torch is None:
+        import torch as t
+        _LIB = load_library()
+        torch = t
+
+
+def _elsewhere(dev, stream) -> bool:
+    """Whether the call needs a guard: another device is current, or a stream was given."""
+    if torch is None:
+        _ready()
+    return stream is not None or torch._C._cuda_getDevice() != dev.index
+
+
+class _Guard:
+    """Makes a device, and a stream on it, current."""
 
     def __init__(self, device, stream):
-        import torch
-        self.device = device
-        self.guards = []
-        if torch.cuda.current_device() != device.index:
-            self.guards.append(torch.cuda.device(device))
-        if stream is not None:
-            self.guards.append(torch.cuda.stream(stream))
-        else:
-            stream = torch.cuda.current_stream(device)
-        self.ptr = stream.cuda_stream
+        self.guards = [torch.cuda.device(device)] + ([torch.cuda.stream(stream)] if stream is not None else [])
 
     def __enter__(self):
         for g in self.guards:
             g.__enter__()
-        return self
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
             g.__exit__(*exc)
 
 
+def _cuda(t, name):
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a CUDA device")
+    return t.device
+
+
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
 def _status_ptr(status, device):
-    import torch
     if status is not None:
         if status.dtype != torch.int32 or status.device != device or status.numel() < 1:
             raise ValueError("status must be an int32 tensor on the cache's device")
@@ -72,18 +92,27 @@ def _status_ptr(status, device):
     return word.data_ptr()
 
 
-def _int32(t, name, device, *shape):
-    """A contiguous int32 tensor on `device` of the given shape (None: any extent)."""
-    import torch
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor on {device}")
-    if t.dim() != len(shape) or any(want is not None and int(have) != want for have, want in zip(t.shape, shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+def _int32(t, name, device, shape):
+    """Pointer of a contiguous int32 tensor of the given shape on `device`."""
+    if t.dtype is not torch.int32 or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
     return t.data_ptr()
 
 
-def _indptr(q_indptr, batch, device):
-    return None if q_indptr is None else _int32(q_indptr, "q_indptr", device, batch + 1)
+def _cache_struct(cache):
+    """cache.c_struct(), reused while the cache holds the same tensors at the same addresses."""
+    kept = cache.__dict__.get("_spec_struct")
+    if kept is not None:
+        k, v, lens, table, max_len, c = kept
+        if k is cache.k and v is cache.v and lens is cache.seq_lens and table is cache.page_table and \
+                max_len == cache.max_seq_len and c.k == k.data_ptr() and c.v == v.data_ptr() and \
+                c.seq_lens == lens.data_ptr() and (table is None or c.page_table == table.data_ptr()):
+            return c
+    if cache.k.device.type != "cuda":
+        raise ValueError("the cache must be on a CUDA device")
+    c = cache.c_struct()
+    cache.__dict__["_spec_struct"] = (cache.k, cache.v, cache.seq_lens, cache.page_table, cache.max_seq_len, c)
+    return c
 
 
 class RotaryEmbedding:
@@ -118,16 +147,14 @@ class RotaryEmbedding:
         return float(self.c.mscale)
 
 
-def _rows(t, name, heads, dtype, device, tokens):
+def _rows(t, name, shape, dtype, device):
     """[T, heads, 128] rows whose heads are 128 apart; returns (pointer, elements from token to token)."""
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != 128 or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be a [{tokens}, heads, 128] {dtype} tensor on {device}")
-    if heads is not None and t.shape[1] != heads:
-        raise ValueError(f"{name} must have {heads} heads")
-    st = t.stride()
-    if st[2] != 1 or (t.shape[1] > 1 and st[1] != 128):
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{name} must be a {tuple(shape)} {dtype} tensor on {device}")
+    a, b, c = t.stride()
+    if c != 1 or (b != 128 and shape[1] > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), (st[0] if tokens > 1 else int(t.shape[1]) * 128)
+    return t.data_ptr(), a if shape[0] > 1 else shape[1] * 128
 
 
 def rope_append(cache: KVCache, rope: RotaryEmbedding, q, k, v, q_indptr=None, max_tokens_per_seq: int = 1,
@@ -139,30 +166,40 @@ def rope_append(cache: KVCache, rope: RotaryEmbedding, q, k, v, q_indptr=None, m
     `positions` (int32 [T]) if given, at seq_lens[b] - n_b + depth (int32 [T], as tree_mask returns) if
     given, else at its cache position.  Returns the rotated queries ([T, Hq, 128], contiguous; `out_q`
     may be q itself)."""
-    import torch
-    dev = cache.device
-    with _Call(dev, stream) as call:
-        T, Hq = int(q.shape[0]), int(q.shape[1])
-        if q.dtype not in (torch.bfloat16, torch.float32):
-            raise TypeError("q must be bfloat16 or float32")
-        c = _QueriesC()
-        c.q, q_stride = _rows(q, "q", None, q.dtype, dev, T)
-        kp, k_stride = _rows(k, "k", cache.num_kv_heads, q.dtype, dev, T)
-        vp, v_stride = _rows(v, "v", cache.num_kv_heads, q.dtype, dev, T)
-        c.q_dtype = TSD_BF16 if q.dtype == torch.bfloat16 else TSD_F32
-        c.num_q_heads, c.num_tokens = Hq, T
-        c.q_indptr = _indptr(q_indptr, cache.batch, dev)
-        c.max_tokens_per_seq = 1 if q_indptr is None else int(max_tokens_per_seq)
-        c.causal, c.sm_scale = 1, 1.0
-        if out_q is None:
-            out_q = torch.empty((T, Hq, 128), dtype=q.dtype, device=dev)
-        elif out_q.shape != q.shape or out_q.dtype != q.dtype or out_q.device != dev or not out_q.is_contiguous():
-            raise ValueError("out_q must be a contiguous tensor of q's shape and type")
-        _check(load_library().tsd_rope_append(
-            ctypes.byref(cache.c_struct()), ctypes.byref(c), ctypes.byref(rope.c), q_stride, kp, k_stride, vp, v_stride,
-            None if positions is None else _int32(positions, "positions", dev, T),
-            None if depth is None else _int32(depth, "depth", dev, T), out_q.data_ptr(), _status_ptr(status, dev),
-            call.ptr), "tsd_rope_append")
+    dev = _cuda(cache.k, "the cache")
+    if _elsewhere(dev, stream):
+        with _Guard(dev, stream):
+            return rope_append(cache, rope, q, k, v, q_indptr, max_tokens_per_seq, positions, depth, out_q, status)
+    dtype = q.dtype
+    if dtype is torch.bfloat16:
+        code = TSD_BF16
+    elif dtype is torch.float32:
+        code = TSD_F32
+    else:
+        raise TypeError("q must be bfloat16 or float32")
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, 128]")
+    T, Hq, _ = q.shape
+    kv = (T, cache.k.shape[1], 128)
+    qp, q_stride = _rows(q, "q", (T, Hq, 128), dtype, dev)
+    kp, k_stride = _rows(k, "k", kv, dtype, dev)
+    vp, v_stride = _rows(v, "v", kv, dtype, dev)
+    cs = _cache_struct(cache)
+    if q_indptr is None:
+        ip, max_tokens_per_seq = None, 1
+    else:
+        ip = _int32(q_indptr, "q_indptr", dev, (cs.batch + 1,))
+    c = _QueriesC(qp, code, Hq, T, ip, int(max_tokens_per_seq), 1, 1.0)
+    if out_q is None:
+        out_q = torch.empty((T, Hq, 128), dtype=dtype, device=dev)
+    elif out_q.shape != q.shape or out_q.dtype is not dtype or out_q.device != dev or not out_q.is_contiguous():
+        raise ValueError("out_q must be a contiguous tensor of q's shape and type")
+    st = _LIB.tsd_rope_append(cs, c, rope.c, q_stride, kp, k_stride, vp, v_stride,
+                              None if positions is None else _int32(positions, "positions", dev, (T,)),
+                              None if depth is None else _int32(depth, "depth", dev, (T,)), out_q.data_ptr(),
+                              _status_ptr(status, dev), _raw_stream(dev))
+    if st:
+        raise TsdError(st, "tsd_rope_append")
     return out_q
 
 
@@ -170,23 +207,26 @@ def tree_mask(parents, q_indptr=None, max_tokens_per_seq: int = 1, mask=None, de
     """Ancestors of drafted tokens (tsd_tree_mask): parents int32 [T], each the index of an earlier draft of
     the same sequence or -1.  Returns (mask int32 [T, ceil(max_tokens_per_seq / 32)] of bits, depth
     int32 [T])."""
-    import torch
-    dev = parents.device
-    if dev.type != "cuda":
-        raise ValueError("parents must be on a CUDA device")
-    with _Call(dev, stream) as call:
-        T = int(parents.shape[0])
-        pp = _int32(parents, "parents", dev, T)
-        batch = T if q_indptr is None else int(q_indptr.shape[0]) - 1
-        n = 1 if q_indptr is None else int(max_tokens_per_seq)
-        W = (n + 31) // 32
-        if mask is None:
-            mask = torch.empty((T, W), dtype=torch.int32, device=dev)
-        if depth is None:
-            depth = torch.empty((T,), dtype=torch.int32, device=dev)
-        _check(load_library().tsd_tree_mask(batch, _indptr(q_indptr, batch, dev), T, n, pp,
-                                            _int32(mask, "mask", dev, T, W), _int32(depth, "depth", dev, T),
-                                            _status_ptr(status, dev), call.ptr), "tsd_tree_mask")
+    dev = _cuda(parents, "parents")
+    if _elsewhere(dev, stream):
+        with _Guard(dev, stream):
+            return tree_mask(parents, q_indptr, max_tokens_per_seq, mask, depth, status)
+    T = parents.shape[0]
+    pp = _int32(parents, "parents", dev, (T,))
+    if q_indptr is None:
+        batch, n, ip = T, 1, None
+    else:
+        batch, n = q_indptr.shape[0] - 1, int(max_tokens_per_seq)
+        ip = _int32(q_indptr, "q_indptr", dev, (batch + 1,))
+    W = (n + 31) // 32
+    if mask is None:
+        mask = torch.empty((T, W), dtype=torch.int32, device=dev)
+    if depth is None:
+        depth = torch.empty((T,), dtype=torch.int32, device=dev)
+    st = _LIB.tsd_tree_mask(batch, ip, T, n, pp, _int32(mask, "mask", dev, (T, W)), _int32(depth, "depth", dev, (T,)),
+                            _status_ptr(status, dev), _raw_stream(dev))
+    if st:
+        raise TsdError(st, "tsd_tree_mask")
     return mask, depth
 
 
@@ -197,51 +237,54 @@ def tree_decode(cache: KVCache, queries: Queries, mask=None, out=None, out_dtype
     mask: int32 [T, ceil(max_tokens_per_seq / 32)], bit i of a row for draft i of the sequence, or None
     for a chain of drafts.  Returns (out [T, Hq, 128], lse [T, Hq] or None); a draft that sees nothing
     gets out 0 and lse -inf.  workspace: scratch to reuse; by default it is allocated per call."""
-    import torch
-    lib = load_library()
-    dev = cache.device
+    dev = _cuda(cache.k, "the cache")
+    if _elsewhere(dev, stream):
+        with _Guard(dev, stream):
+            return tree_decode(cache, queries, mask, out, out_dtype, lse, workspace, status)
     q = queries.q
-    if q.device != dev or (queries.q_indptr is not None and queries.q_indptr.device != dev):
+    if q.device != dev:
         raise ValueError("tree_decode takes device tensors only")
-    with _Call(dev, stream) as call:
-        _indptr(queries.q_indptr, cache.batch, dev)
-        cs, qs = cache.c_struct(), queries.c_struct()
-        T, Hq = int(q.shape[0]), int(q.shape[1])
-        mp = None
-        if mask is not None:
-            mp = _int32(mask, "mask", dev, T, (qs.max_tokens_per_seq + 31) // 32)
-        if out is None:
-            out = torch.empty((T, Hq, 128), dtype=out_dtype or torch.bfloat16, device=dev)
-        elif tuple(out.shape) != (T, Hq, 128) or out.device != dev or not out.is_contiguous():
-            raise ValueError("out must be a contiguous [T, Hq, 128] tensor on the cache's device")
-        elif out_dtype is not None and out_dtype != out.dtype:
-            raise ValueError("out_dtype disagrees with out")
-        if out.dtype not in (torch.bfloat16, torch.float32):
-            raise TypeError("out must be bfloat16 or float32")
-        if lse is True:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-        elif lse is None or lse is False:
-            lse = None
-        elif tuple(lse.shape) != (T, Hq) or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
-            raise ValueError("lse must be a contiguous float32 [T, Hq] tensor on the cache's device")
-        odt = TSD_BF16 if out.dtype == torch.bfloat16 else TSD_F32
-        nbytes = lib.tsd_tree_decode_workspace_size(ctypes.byref(cs), ctypes.byref(qs), odt)
-        ws, sp = _scratch(workspace, nbytes, ("tree_decode",) + _shape_key(cache, queries), dev, call, status)
-        _check(lib.tsd_tree_decode(ctypes.byref(cs), ctypes.byref(qs), mp, out.data_ptr(), odt,
-                                   None if lse is None else lse.data_ptr(), ws[0], nbytes, sp, call.ptr),
-               "tsd_tree_decode")
+    cs, qs = _cache_struct(cache), queries.c_struct()
+    T, Hq, _ = q.shape
+    if queries.q_indptr is not None:
+        _int32(queries.q_indptr, "q_indptr", dev, (cs.batch + 1,))
+    mp = None if mask is None else _int32(mask, "mask", dev, (T, (qs.max_tokens_per_seq + 31) // 32))
+    if out is None:
+        out = torch.empty((T, Hq, 128), dtype=out_dtype or torch.bfloat16, device=dev)
+    elif out.shape != (T, Hq, 128) or out.device != dev or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [T, Hq, 128] tensor on the cache's device")
+    elif out_dtype is not None and out_dtype != out.dtype:
+        raise ValueError("out_dtype disagrees with out")
+    if out.dtype is torch.bfloat16:
+        code = TSD_BF16
+    elif out.dtype is torch.float32:
+        code = TSD_F32
+    else:
+        raise TypeError("out must be bfloat16 or float32")
+    if lse is True:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    elif lse is None or lse is False:
+        lse = None
+    elif lse.shape != (T, Hq) or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [T, Hq] tensor on the cache's device")
+    nbytes = _LIB.tsd_tree_decode_workspace_size(cs, qs, code)
+    ws, keep, sp = _scratch(workspace, nbytes, "tree_decode", dev, status)
+    st = _LIB.tsd_tree_decode(cs, qs, mp, out.data_ptr(), code, None if lse is None else lse.data_ptr(), ws, nbytes, sp,
+                              _raw_stream(dev))
+    if st:
+        raise TsdError(st, "tsd_tree_decode")
     return out, lse
 
 
-def _scratch(workspace, nbytes, key, dev, call, status):
-    """Scratch of `nbytes` as (pointer, owner), and the status word to use.  A Workspace keeps its status
-    word in its first 256 bytes; the scratch lies behind them."""
-    import torch
+def _scratch(workspace, nbytes, what, dev, status):
+    """Scratch of `nbytes`: its pointer, its owner, and the status word to use.  A Workspace keeps its status
+    word in its first 256 bytes; the scratch lies behind them.  The key is one no other call uses: a call that
+    needs the workspace's first part zeroed finds another key and zeroes it."""
     if workspace is None:
-        buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-        return (buf.data_ptr(), buf), _status_ptr(status, dev)
-    buf = workspace.get(nbytes + 256, key, call.ptr)
-    return (buf.data_ptr() + 256, buf), buf.data_ptr() if status is None else _status_ptr(status, dev)
+        buf = torch.empty(nbytes if nbytes > 256 else 256, dtype=torch.uint8, device=dev)
+        return buf.data_ptr(), buf, _status_ptr(status, dev)
+    buf = workspace.get(nbytes + 256, what, _raw_stream(dev))
+    return buf.data_ptr() + 256, buf, buf.data_ptr() if status is None else _status_ptr(status, dev)
 
 
 class LayerCaches:
@@ -269,7 +312,7 @@ class LayerCaches:
 def _refs(refs, cache, dev):
     if cache.page_table is None:
         raise ValueError("refs go with a paged cache")
-    return _int32(refs, "refs", dev, int(cache.k.shape[0]))
+    return _int32(refs, "refs", dev, (cache.k.shape[0],))
 
 
 def cache_fork(caches, refs, src, dst, status=None, stream=None) -> None:
@@ -277,13 +320,17 @@ def cache_fork(caches, refs, src, dst, status=None, stream=None) -> None:
 
     refs: int32 [num_pages], how many page-table entries hold each page (0: free).  src, dst: int32 [n].
     The cache's page_table and seq_lens and refs are updated in place."""
-    cache = LayerCaches.of(caches).caches[0]
-    dev = cache.device
-    with _Call(dev, stream) as call:
-        n = int(src.shape[0])
-        _check(load_library().tsd_cache_fork(ctypes.byref(cache.c_struct()), _refs(refs, cache, dev), n,
-                                             _int32(src, "src", dev, n), _int32(dst, "dst", dev, n),
-                                             _status_ptr(status, dev), call.ptr), "tsd_cache_fork")
+    caches = LayerCaches.of(caches)
+    cache = caches.caches[0]
+    dev = _cuda(cache.k, "the cache")
+    if _elsewhere(dev, stream):
+        with _Guard(dev, stream):
+            return cache_fork(caches, refs, src, dst, status)
+    n = src.shape[0]
+    st = _LIB.tsd_cache_fork(_cache_struct(cache), _refs(refs, cache, dev), n, _int32(src, "src", dev, (n,)),
+                             _int32(dst, "dst", dev, (n,)), _status_ptr(status, dev), _raw_stream(dev))
+    if st:
+        raise TsdError(st, "tsd_cache_fork")
 
 
 def cache_resize(caches, refs, new_lens, workspace: Optional[Workspace] = None, status=None, stream=None) -> None:
@@ -294,18 +341,20 @@ def cache_resize(caches, refs, new_lens, workspace: Optional[Workspace] = None, 
     the lowest free ones at the start of the call, given out in order of sequence; where they do not
     suffice a sequence stays as it was (DEV_NO_PAGES).  The cache's page_table (-1 where a page was
     released), seq_lens and refs are updated in place."""
-    lib = load_library()
-    layers = LayerCaches.of(caches)
-    cache = layers.caches[0]
-    dev = cache.device
-    with _Call(dev, stream) as call:
-        rp = _refs(refs, cache, dev)
-        np_ = _int32(new_lens, "new_lens", dev, cache.batch)
-        cs = cache.c_struct()
-        nbytes = lib.tsd_cache_resize_workspace_size(ctypes.byref(cs))
-        ws, sp = _scratch(workspace, nbytes, ("cache_resize", cache.batch, int(cache.k.shape[0])), dev, call, status)
-        _check(lib.tsd_cache_resize(ctypes.byref(cs), len(layers.caches), layers.c_layers, rp, np_, ws[0], nbytes, sp,
-                                    call.ptr), "tsd_cache_resize")
+    caches = LayerCaches.of(caches)
+    cache = caches.caches[0]
+    dev = _cuda(cache.k, "the cache")
+    if _elsewhere(dev, stream):
+        with _Guard(dev, stream):
+            return cache_resize(caches, refs, new_lens, workspace, status)
+    rp = _refs(refs, cache, dev)
+    cs = _cache_struct(cache)
+    lens = _int32(new_lens, "new_lens", dev, (cs.batch,))
+    nbytes = _LIB.tsd_cache_resize_workspace_size(cs)
+    ws, keep, sp = _scratch(workspace, nbytes, "cache_resize", dev, status)
+    st = _LIB.tsd_cache_resize(cs, len(caches.caches), caches.c_layers, rp, lens, ws, nbytes, sp, _raw_stream(dev))
+    if st:
+        raise TsdError(st, "tsd_cache_resize")
 
 
 def cache_compact(caches, keep, q_indptr=None, max_tokens_per_seq: int = 1, refs=None, out_lens=None, status=None,
@@ -317,22 +366,29 @@ def cache_compact(caches, keep, q_indptr=None, max_tokens_per_seq: int = 1, refs
     drafts of each sequence (None: one each).  refs: when given, a sequence whose rows to be written lie in
     a shared page is left as it was (DEV_SHARED_PAGE).  Returns the new lengths, int32 [B], to be passed to
     cache_resize; seq_lens itself is not changed."""
-    import torch
-    lib = load_library()
-    layers = LayerCaches.of(caches)
-    cache = layers.caches[0]
-    dev = cache.device
-    with _Call(dev, stream) as call:
-        B = cache.batch
-        if out_lens is None:
-            out_lens = torch.empty((B,), dtype=torch.int32, device=dev)
-        n = 1 if q_indptr is None else int(max_tokens_per_seq)
-        kp = _int32(keep, "keep", dev, B, None)
-        if int(keep.shape[1]) < 1:
-            raise TsdError(TSD_ERR_INVALID_ARGUMENT, "keep must have room for one draft")
-        _check(lib.tsd_cache_compact(ctypes.byref(cache.c_struct()), len(layers.caches), layers.c_layers,
-                                     _indptr(q_indptr, B, dev), n * B, n, kp, int(keep.shape[1]),
-                                     None if refs is None else _refs(refs, cache, dev),
-                                     _int32(out_lens, "out_lens", dev, B), _status_ptr(status, dev), call.ptr),
-               "tsd_cache_compact")
+    caches = LayerCaches.of(caches)
+    cache = caches.caches[0]
+    dev = _cuda(cache.k, "the cache")
+    if _elsewhere(dev, stream):
+        with _Guard(dev, stream):
+            return cache_compact(caches, keep, q_indptr, max_tokens_per_seq, refs, out_lens, status)
+    cs = _cache_struct(cache)
+    B = cs.batch
+    if out_lens is None:
+        out_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+    if keep.dim() != 2:
+        raise ValueError("keep must be [batch, k_max]")
+    k_max = keep.shape[1]
+    if k_max < 1:
+        raise TsdError(TSD_ERR_INVALID_ARGUMENT, "keep must have room for one draft")
+    kp = _int32(keep, "keep", dev, (B, k_max))
+    if q_indptr is None:
+        n, ip = 1, None
+    else:
+        n, ip = int(max_tokens_per_seq), _int32(q_indptr, "q_indptr", dev, (B + 1,))
+    st = _LIB.tsd_cache_compact(cs, len(caches.caches), caches.c_layers, ip, n * B, n, kp, k_max,
+                                None if refs is None else _refs(refs, cache, dev),
+                                _int32(out_lens, "out_lens", dev, (B,)), _status_ptr(status, dev), _raw_stream(dev))
+    if st:
+        raise TsdError(st, "tsd_cache_compact")
     return out_lens
