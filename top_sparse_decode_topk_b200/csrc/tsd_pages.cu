@@ -70,26 +70,31 @@ __global__ void __launch_bounds__(256) cache_fork_kernel(Pool p, int num_pairs, 
 // ---------------------------------------------------------------------------
 // Resize
 // ---------------------------------------------------------------------------
-// One cluster of kRzCtas CTAs does the bookkeeping in four steps with cluster barriers between, so
+// One cluster of kRzCtas CTAs does the bookkeeping in three steps with cluster barriers between, so
 // that a call is one launch (and one more for the copies) with no grid-wide wait:
-//   1  every warp counts the free pages of its slice of refs; CTA 0 also finds what every
-//      sequence wants and the running sums of that;
+//   1  CTA 0 finds what every sequence wants and the running sums of that; every warp of the others
+//      counts the free pages of its slice of refs, keeping the first kRzKept groups' as bits;
 //   2  the warps whose first free page has a rank below the total wanted list their free pages;
 //   3  a warp per sequence hands out the listed pages, updates its row and the counts.
-// Sequences are served from the list in order, so the outcome does not depend on timing.
+// Sequences are served from the list in order, so the outcome does not depend on timing.  A call
+// is a chain of dependent loads (length, page, count; listed page, row) more than it is bytes.
 constexpr int kRzCtas = 8;
 constexpr int kRzThreads = 1024;
 constexpr int kRzWarps = kRzCtas * kRzThreads / 32;
+constexpr int kRzCounters = (kRzCtas - 1) * kRzThreads / 32;   // warps that count
+constexpr int kRzRelease = 8;
+constexpr int kRzKept = 8;                                     // groups of 128 pages: 4 bits a lane each
 
 struct ResizeArgs {
   Pool p;
   const int32_t* new_lens;
-  int32_t* counts;   // [kRzWarps] free pages of each warp's slice
+  int32_t* counts;   // [kRzCounters] free pages of each warp's slice
   int32_t* total;    // [1] pages wanted in all
   int2* want;        // [batch] (first rank, pages wanted | copy flag << 31); -1 first: leave alone
   int2* pairs;       // [batch] (from, to) page to copy, (-1, -1) for none
   int32_t* list;     // [num_pages] the free pages of ranks below the total
   uint32_t* status;
+  int32_t aligned;   // refs is 16-byte aligned
 };
 
 __device__ __forceinline__ void cluster_sync() {
@@ -109,25 +114,29 @@ __device__ __forceinline__ int warp_exclusive(int v, int lane) {
   return x - v;
 }
 
+// Which of pages at .. at + 3 are free, as bits.
+__device__ __forceinline__ uint32_t free_bits(const Pool& p, int64_t at, bool aligned) {
+  uint32_t bits = 0;
+  if (aligned && at + 4 <= p.num_pages) {
+    const int4 r = *reinterpret_cast<const int4*>(p.refs + at);
+    return (uint32_t)(r.x == 0) | (uint32_t)(r.y == 0) << 1 | (uint32_t)(r.z == 0) << 2 | (uint32_t)(r.w == 0) << 3;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (at + e < p.num_pages && p.refs[at + e] == 0) bits |= 1u << e;
+  return bits;
+}
+
 __global__ void __cluster_dims__(kRzCtas, 1, 1) __launch_bounds__(kRzThreads) cache_resize_kernel(ResizeArgs a) {
   __shared__ int tmp[kRzThreads / 32 + 1];
-  __shared__ int s_counts[kRzWarps];
   const Pool& p = a.p;
   const int tid = threadIdx.x, lane = tid & 31;
   const int gw = blockIdx.x * (kRzThreads / 32) + (tid >> 5);
+  const int cw = gw - kRzThreads / 32;   // this warp among those that count
   pdl_launch_dependents();
-  // ---- 1: slices of whole 128-page groups, so that lane l takes pages 4l .. 4l + 3 of a group
-  const int64_t groups = (p.num_pages + 127) / 128;
-  const int64_t g0 = groups * gw / kRzWarps, g1 = groups * (gw + 1) / kRzWarps;
-  int free_cnt = 0;
-  for (int64_t g = g0; g < g1; ++g) {
-    const int64_t at = g * 128 + 4 * lane;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (at + e < p.num_pages) free_cnt += p.refs[at + e] == 0;
-  }
-  free_cnt = warp_sum(free_cnt);
-  if (lane == 0) a.counts[gw] = free_cnt;
+  // ---- 1: slices of whole 128-page groups, lane l taking pages 4l .. 4l + 3 of a group
+  int64_t g0 = 0, g1 = 0;
+  uint32_t kept = 0;
   if (blockIdx.x == 0) {
     int running = 0;
     for (int b0 = 0; b0 < p.batch; b0 += kRzThreads) {
@@ -155,25 +164,37 @@ __global__ void __cluster_dims__(kRzCtas, 1, 1) __launch_bounds__(kRzThreads) ca
       if (b < p.batch) a.want[b] = make_int2(ok ? first : -1, (need + cow) | (cow << 31));
     }
     if (tid == 0) *a.total = running;
+  } else {
+    const int64_t groups = (p.num_pages + 127) / 128;
+    g0 = groups * cw / kRzCounters;
+    g1 = groups * (cw + 1) / kRzCounters;
+    int free_cnt = 0;
+#pragma unroll
+    for (int k = 0; k < kRzKept; ++k)
+      if (g0 + k < g1) kept |= free_bits(p, (g0 + k) * 128 + 4 * lane, a.aligned) << (4 * k);
+    free_cnt = __popc(kept);
+#pragma unroll 4
+    for (int64_t g = g0 + kRzKept; g < g1; ++g) free_cnt += __popc(free_bits(p, g * 128 + 4 * lane, a.aligned));
+    free_cnt = warp_sum(free_cnt);
+    if (lane == 0) a.counts[cw] = free_cnt;
   }
   cluster_sync();
   // ---- 2
-  for (int i = tid; i < kRzWarps; i += kRzThreads) s_counts[i] = a.counts[i];
-  __syncthreads();
   const int total = *a.total;
+  int2 w = gw < p.batch ? a.want[gw] : make_int2(-1, 0);   // step 3's first sequence
+  int old = gw < p.batch ? p.lens[gw] : 0, now = gw < p.batch ? a.new_lens[gw] : 0;
   int before = 0, free_all = 0;
-  for (int i = lane; i < kRzWarps; i += 32) {
-    free_all += s_counts[i];
-    if (i < gw) before += s_counts[i];
+#pragma unroll
+  for (int i = lane; i < kRzCounters; i += 32) {
+    const int c = a.counts[i];
+    free_all += c;
+    if (i < cw) before += c;
   }
   before = warp_sum(before);
   free_all = warp_sum(free_all);
   for (int64_t g = g0; g < g1 && before < total; ++g) {
     const int64_t at = g * 128 + 4 * lane;
-    uint32_t is_free = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (at + e < p.num_pages && p.refs[at + e] == 0) is_free |= 1u << e;
+    const uint32_t is_free = g - g0 < kRzKept ? kept >> (4 * (int)(g - g0)) & 15u : free_bits(p, at, a.aligned);
     const int mine = __popc(is_free);
     int rank = before + warp_exclusive(mine, lane);
     before += warp_sum(mine);
@@ -187,14 +208,16 @@ __global__ void __cluster_dims__(kRzCtas, 1, 1) __launch_bounds__(kRzThreads) ca
   cluster_sync();
   // ---- 3
   for (int b = gw; b < p.batch; b += kRzWarps) {
-    const int2 w = a.want[b];
+    if (b != gw) {
+      w = a.want[b];
+      old = p.lens[b];
+      now = a.new_lens[b];
+    }
     int2 pair = make_int2(-1, -1);
     if (w.x >= 0) {
       const int need = w.y & 0x7fffffff, cow = (int)((uint32_t)w.y >> 31);
-      const int old = p.lens[b], now = a.new_lens[b];
       const int have = pages_of(old, p.page_shift), end = pages_of(now, p.page_shift);
       int32_t* row = p.table + (int64_t)b * p.max_pages;
-      __syncwarp();
       if (need > 0 && (int64_t)w.x + need > free_all) {
         if (lane == 0) flag_optional(a.status, TSD_DEV_NO_PAGES);
       } else {
@@ -212,16 +235,30 @@ __global__ void __cluster_dims__(kRzCtas, 1, 1) __launch_bounds__(kRzThreads) ca
           row[i] = page;
           p.refs[page] = 1;
         }
-        for (int i = end + lane; i < have; i += 32) {
-          const int32_t page = row[i];
-          row[i] = -1;
-          if (page < 0 || (int64_t)page >= p.num_pages) {
-            flag_optional(a.status, TSD_DEV_BAD_PAGE);
-          } else if (atomicSub(p.refs + page, 1) < 1) {   // it was free already
-            atomicAdd(p.refs + page, 1);
-            flag_optional(a.status, TSD_DEV_BAD_PAGE);
+        // eight rounds' loads, then their counts, at once: an ended sequence gives back hundreds of pages
+        for (int i0 = end + lane; i0 < have; i0 += 32 * kRzRelease) {
+          int32_t page[kRzRelease], held[kRzRelease];
+#pragma unroll
+          for (int e = 0; e < kRzRelease; ++e) {
+            page[e] = i0 + 32 * e < have ? row[i0 + 32 * e] : 0;
+            held[e] = 1;
+          }
+#pragma unroll
+          for (int e = 0; e < kRzRelease; ++e) {
+            if (i0 + 32 * e >= have) continue;
+            row[i0 + 32 * e] = -1;
+            if (page[e] < 0 || (int64_t)page[e] >= p.num_pages) flag_optional(a.status, TSD_DEV_BAD_PAGE);
+            else held[e] = atomicSub(p.refs + page[e], 1);
+          }
+#pragma unroll
+          for (int e = 0; e < kRzRelease; ++e) {
+            if (held[e] < 1) {   // it was free already
+              atomicAdd(p.refs + page[e], 1);
+              flag_optional(a.status, TSD_DEV_BAD_PAGE);
+            }
           }
         }
+        __syncwarp();
         if (lane == 0) p.lens[b] = now;
       }
     }
@@ -273,7 +310,7 @@ __global__ void __launch_bounds__(kCpThreads) page_copy_kernel(const __grid_cons
 // row that is still to be read.  Nothing has to be staged and streams need not wait for one another.
 constexpr int kCmThreads = 256;
 constexpr int kCmStreams = kCmThreads / 16;
-constexpr int kCmBatch = 8;
+constexpr int kCmBatch = 4;
 constexpr int kCmPart = 256;   // list entries resolved to rows at a time
 
 struct CompactArgs {
@@ -297,7 +334,7 @@ __device__ __forceinline__ int64_t position_row(const KvView& kv, int b, int r, 
   return (((int64_t)*page * kv.hkv) << kv.page_shift) | (r & ((1 << kv.page_shift) - 1));
 }
 
-__global__ void __launch_bounds__(kCmThreads) cache_compact_kernel(const __grid_constant__ CompactArgs a,
+__global__ void __launch_bounds__(kCmThreads, 7) cache_compact_kernel(const __grid_constant__ CompactArgs a,
                                                                    const __grid_constant__ Layers layers) {
   __shared__ int64_t s_src[kCmPart], s_dst[kCmPart];
   __shared__ int s_cnt;
@@ -309,6 +346,9 @@ __global__ void __launch_bounds__(kCmThreads) cache_compact_kernel(const __grid_
     s_bad = 0;
   }
   __syncthreads();
+  const int32_t* keep = a.keep + (int64_t)b * a.k_max;
+  // the first part of the list does not wait for the descriptor
+  int r = tid < a.k_max ? __ldg(keep + tid) : -1, prev = tid > 0 && tid < a.k_max ? __ldg(keep + tid - 1) : -1;
   const int len = __ldg(a.kv.seq_lens + b);
   const int t0 = a.q_indptr != nullptr ? __ldg(a.q_indptr + b) : b;
   const int t1 = a.q_indptr != nullptr ? __ldg(a.q_indptr + b + 1) : b + 1;
@@ -321,26 +361,32 @@ __global__ void __launch_bounds__(kCmThreads) cache_compact_kernel(const __grid_
     return;
   }
   // every block checks the whole list, so that all streams of a sequence move or none
-  const int32_t* keep = a.keep + (int64_t)b * a.k_max;
   uint32_t bad = 0;
   int cnt = 0;
   for (int i = tid; i < a.k_max; i += kCmThreads) {
-    const int r = __ldg(keep + i);
-    const int prev = i > 0 ? __ldg(keep + i - 1) : -1;
+    if (i != tid) {
+      r = __ldg(keep + i);
+      prev = __ldg(keep + i - 1);
+    }
+    int64_t from = -1, to = -1;
     if (r < 0) {
       if (r != -1) bad |= TSD_DEV_BAD_INDEX;
-      continue;
+    } else {
+      ++cnt;
+      if (r >= n || r <= prev || (i > 0 && prev < 0)) {
+        bad |= TSD_DEV_BAD_INDEX;
+      } else if (r != i) {   // else it stays where it is
+        int32_t ps, pd;
+        from = position_row(a.kv, b, base + r, &ps);
+        to = position_row(a.kv, b, base + i, &pd);
+        if (from < 0 || to < 0) bad |= TSD_DEV_BAD_PAGE;
+        else if (a.refs != nullptr && pd >= 0 && __ldg(a.refs + pd) > 1) bad |= TSD_DEV_SHARED_PAGE;
+      }
     }
-    ++cnt;
-    if (r >= n || r <= prev || (i > 0 && prev < 0)) {
-      bad |= TSD_DEV_BAD_INDEX;
-      continue;
+    if (i < kCmPart) {   // kCmPart = kCmThreads: the first part of the list, resolved
+      s_src[i] = from;
+      s_dst[i] = to;
     }
-    if (r == i) continue;   // stays where it is
-    int32_t ps, pd;
-    const int64_t from = position_row(a.kv, b, base + r, &ps), to = position_row(a.kv, b, base + i, &pd);
-    if (from < 0 || to < 0) bad |= TSD_DEV_BAD_PAGE;
-    else if (a.refs != nullptr && pd >= 0 && __ldg(a.refs + pd) > 1) bad |= TSD_DEV_SHARED_PAGE;
   }
   if (cnt) atomicAdd(&s_cnt, cnt);
   if (bad) atomicOr(&s_bad, bad);
@@ -363,14 +409,16 @@ __global__ void __launch_bounds__(kCmThreads) cache_compact_kernel(const __grid_
   uint4* rows = static_cast<uint4*>(which ? layers.v[layer] : layers.k[layer]) + g * head_rows * 16 + col;
   for (int i0 = 0; i0 < total; i0 += kCmPart) {
     const int m = min(kCmPart, total - i0);
-    __syncthreads();
-    for (int i = tid; i < m; i += kCmThreads) {
-      const int r = __ldg(keep + i0 + i);
-      int32_t page;
-      s_src[i] = r == i0 + i ? -1 : position_row(a.kv, b, base + r, &page);
-      s_dst[i] = position_row(a.kv, b, base + i0 + i, &page);
+    if (i0 > 0) {
+      __syncthreads();
+      for (int i = tid; i < m; i += kCmThreads) {
+        const int kr = __ldg(keep + i0 + i);
+        int32_t page;
+        s_src[i] = kr == i0 + i ? -1 : position_row(a.kv, b, base + kr, &page);
+        s_dst[i] = position_row(a.kv, b, base + i0 + i, &page);
+      }
+      __syncthreads();
     }
-    __syncthreads();
     if (!live) continue;
     for (int i = 0; i < m; i += kCmBatch) {
       uint4 x[kCmBatch];
@@ -420,7 +468,7 @@ struct ResizeLayout {
 static ResizeLayout resize_layout(int64_t batch, int64_t num_pages) {
   ResizeLayout l;
   l.counts = 0;
-  l.total_off = kRzWarps * sizeof(int32_t);
+  l.total_off = kRzCounters * sizeof(int32_t);
   l.want = align256(l.total_off + sizeof(int32_t));
   l.pairs = l.want + align256((size_t)batch * sizeof(int2));
   l.list = l.pairs + align256((size_t)batch * sizeof(int2));
@@ -475,6 +523,7 @@ tsd_status tsd_cache_resize(const tsd_kv_cache* cache, int32_t num_layers, const
   a.pairs = reinterpret_cast<int2*>(w + l.pairs);
   a.list = reinterpret_cast<int32_t*>(w + l.list);
   a.status = status;
+  a.aligned = ((uintptr_t)refs & 15) == 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cache_resize_kernel<<<kRzCtas, kRzThreads, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();

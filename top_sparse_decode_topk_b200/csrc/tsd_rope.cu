@@ -34,7 +34,7 @@ struct RopeArgs {
   int32_t toks;     // tokens per block
 };
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeMaxToks = 4;
 
 // Eight consecutive elements as fp32.

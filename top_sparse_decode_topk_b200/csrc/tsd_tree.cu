@@ -1038,21 +1038,22 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 }
 
 // Merge of the partial states of units cut over several CTAs, in the order of the shares.  One block
-// per 32 lists of a (sequence, kv head) and kTgDims of their dims; a lane per list, so that the
-// states' rows are read whole.  The warps first find the shares' weights, which stay in shared memory,
-// then take four dims each, in two halves of the shares: few lists with many shares (one short step of
-// one user: 65 shares) need many loads under way.
+// per 32 lists of a (sequence, kv head) and 16 ND of their dims; a lane per list, so that the states'
+// rows are read whole.  The warps find the weights of kTgShares shares at a time, which they keep in
+// shared memory, then take 4 ND dims each, in two halves of the shares, with eight rows under way: a
+// short step of one user has 33 shares to merge and few lists to do it with (ND = 1), a batch has more
+// blocks than the SMs hold, each with its chain of dependent loads (ND = 4).
 constexpr int kTgThreads = 256;
-constexpr int kTgDims = 16;
 constexpr int kTgWarps = kTgThreads / 32;
+constexpr int kTgShares = 32;
 
-template <int QP, int PP>
+template <int QP, int PP, int ND>
 __global__ void __launch_bounds__(kTgThreads) tree_merge_kernel(const __grid_constant__ TreeArgs a, int groups) {
   using SH = TreeShape<QP, PP>;
-  extern __shared__ float tg_w[];   // [shares of the unit][32]
+  __shared__ float weight[kTgShares][32];
   __shared__ float red[kTgWarps][32];
-  __shared__ float4 half[4][32];
-  constexpr int kSlices = kHeadDim / kTgDims;
+  __shared__ float4 half[4 * ND][32];
+  constexpr int kSlices = 8 / ND, kAhead = 8 / ND;
   const int slice = blockIdx.x % kSlices, unit = blockIdx.x / kSlices;
   const int rg = unit % groups, g = (unit / groups) % a.kv.hkv, b = unit / groups / a.kv.hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1071,57 +1072,82 @@ __global__ void __launch_bounds__(kTgThreads) tree_merge_kernel(const __grid_con
   const int row = min(prow, a.part_rows - 1);
   // the first share of the unit starts at its first tile: its state is in the odd slot
   auto slot = [&](int p) { return 2 * (int64_t)(c0 + p) + (p == 0 ? 1 : 0); };
+  // the first rows are on their way while the weights are found
+  const int d4 = slice * 4 * ND + (warp & 3), p0 = warp >> 2;   // and every fourth after it
+  float4 x[kAhead][ND];
+  auto ask = [&](int q) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+        if (q + 2 * i < parts) x[i][d] = __ldcg(a.part_acc + (slot(q + 2 * i) * 32 + d4 + 4 * d) * a.part_rows + row);
+  };
+  ask(p0);
   float m = -INFINITY;
-#pragma unroll 4
-  for (int p = warp; p < parts; p += kTgWarps) {
-    const float x = valid ? __ldcg(&a.part_ml[slot(p) * a.part_rows + row].x) : -INFINITY;
-    tg_w[p * 32 + lane] = x;
-    m = fmaxf(m, x);
-  }
+#pragma unroll 2
+  for (int p = warp; p < parts; p += kTgWarps) m = fmaxf(m, __ldcg(&a.part_ml[slot(p) * a.part_rows + row].x));
   red[warp][lane] = m;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kTgWarps; ++w) m = fmaxf(m, red[w][lane]);
-  __syncthreads();
   float l = 0.f;
-#pragma unroll 4
-  for (int p = warp; p < parts; p += kTgWarps) {
-    const float x = tg_w[p * 32 + lane];
-    const float w = x == -INFINITY ? 0.f : (x == m ? 1.f : fast_exp2(x - m));
-    tg_w[p * 32 + lane] = w;
-    if (x != -INFINITY) l += w * __ldcg(&a.part_ml[slot(p) * a.part_rows + row].y);
+  float4 o[ND];
+#pragma unroll
+  for (int d = 0; d < ND; ++d) o[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < parts; s0 += kTgShares) {
+    const int s1 = min(parts, s0 + kTgShares);
+    if (s0 > 0) __syncthreads();
+#pragma unroll 2
+    for (int p = s0 + warp; p < s1; p += kTgWarps) {
+      const float2 ml = __ldcg(a.part_ml + slot(p) * a.part_rows + row);
+      const float w = ml.x == -INFINITY ? 0.f : (ml.x == m ? 1.f : fast_exp2(ml.x - m));
+      weight[p - s0][lane] = w;
+      if (ml.x != -INFINITY) l += w * ml.y;
+    }
+    __syncthreads();
+    for (int q = s0 + p0; q < s1; q += 2 * kAhead) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const float w = q + 2 * i < s1 ? weight[q + 2 * i - s0][lane] : 0.f;
+        if (w != 0.f) {   // a share in which the list saw nothing holds no numbers
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            o[d].x += w * x[i][d].x;
+            o[d].y += w * x[i][d].y;
+            o[d].z += w * x[i][d].z;
+            o[d].w += w * x[i][d].w;
+          }
+        }
+      }
+      ask(q + 2 * kAhead);
+    }
   }
-  red[warp][lane] = l;
   __syncthreads();
+  red[warp][lane] = l;
+  if (warp >= 4) {
+#pragma unroll
+    for (int d = 0; d < ND; ++d) half[(warp - 4) * ND + d][lane] = o[d];
+  }
+  __syncthreads();
+  if (warp >= 4 || !valid) return;
   l = 0.f;
 #pragma unroll
   for (int w = 0; w < kTgWarps; ++w) l += red[w][lane];
-  const int d4 = slice * (kTgDims / 4) + (warp & 3);
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int p = warp >> 2; p < parts; p += 2) {
-    const float w = tg_w[p * 32 + lane];
-    const float4 x = __ldcg(a.part_acc + (slot(p) * 32 + d4) * a.part_rows + row);
-    if (w != 0.f) {   // a share in which the list saw nothing holds no numbers
-      o.x += w * x.x;
-      o.y += w * x.y;
-      o.z += w * x.z;
-      o.w += w * x.w;
-    }
-  }
-  if (warp >= 4) half[warp - 4][lane] = o;
-  __syncthreads();
-  if (warp >= 4 || !valid) return;
-  const float4 y = half[warp][lane];
   const float norm = l == 0.f ? 0.f : 1.f / l;
-  o = make_float4((o.x + y.x) * norm, (o.y + y.y) * norm, (o.z + y.z) * norm, (o.w + y.w) * norm);
   const int j = list / G;
-  const int64_t lst = (int64_t)(sq.t0 + j) * a.qv.hq + g * G + (list - j * G), at = lst * 32 + d4;
-  if (a.out_f32) static_cast<float4*>(a.out)[at] = o;
-  else static_cast<uint2*>(a.out)[at] = make_uint2(cvt_bf16x2(o.x, o.y), cvt_bf16x2(o.z, o.w));
+  const int64_t lst = (int64_t)(sq.t0 + j) * a.qv.hq + g * G + (list - j * G);
+#pragma unroll
+  for (int d = 0; d < ND; ++d) {
+    const float4 y = half[warp * ND + d][lane];
+    const float4 z = make_float4((o[d].x + y.x) * norm, (o[d].y + y.y) * norm, (o[d].z + y.z) * norm, (o[d].w + y.w) * norm);
+    const int64_t at = lst * 32 + d4 + 4 * d;
+    if (a.out_f32) static_cast<float4*>(a.out)[at] = z;
+    else static_cast<uint2*>(a.out)[at] = make_uint2(cvt_bf16x2(z.x, z.y), cvt_bf16x2(z.z, z.w));
+  }
   if (warp == 0 && slice == 0 && a.lse != nullptr)
     a.lse[lst] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
+static_assert(kTgShares % 16 == 0, "rows asked for ahead run on into the next shares");
 
 struct TreeLayout {
   size_t line, ml, acc, sums, total;
@@ -1147,8 +1173,10 @@ static cudaError_t launch_tree(const TreeArgs& a, const KvMaps& maps, int64_t ba
   tree_decode_kernel<QP, PP><<<a.ctas, kTaThreads, kTaSmem, stream>>>(a, maps);
   const cudaError_t e2 = cudaGetLastError();
   if (e2 != cudaSuccess) return e2;
-  return launch_dependent(tree_merge_kernel<QP, PP>, dim3((unsigned)(batch * a.kv.hkv * groups * (kHeadDim / kTgDims))),
-                          dim3(kTgThreads), (size_t)a.ctas * 32 * sizeof(float), stream, a, groups);
+  const int64_t units = batch * a.kv.hkv * groups;
+  if (units * 8 > a.ctas)   // 2 units: 18.4 us of a step with ND = 1, 20.8 with 4; 128 units: 178.6 and 174.4
+    return launch_dependent(tree_merge_kernel<QP, PP, 4>, dim3((unsigned)(units * 2)), dim3(kTgThreads), 0, stream, a, groups);
+  return launch_dependent(tree_merge_kernel<QP, PP, 1>, dim3((unsigned)(units * 8)), dim3(kTgThreads), 0, stream, a, groups);
 }
 
 }  // namespace tsd
