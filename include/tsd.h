@@ -436,7 +436,8 @@ tsd_status tsd_topk_select_label(const tsd_kv_cache* cache, const void* label_k,
  *
  * As everywhere in this header, seq_lens[b] counts the n_b new tokens of the step, which are the
  * last n_b tokens of the sequence: new token j sits at cache position seq_lens[b] - n_b + j.
- * Shape arguments work as in tsd_queries (q_indptr NULL: one new token per sequence).  A sequence
+ * Shape arguments work as in tsd_queries (q_indptr NULL: one new token per sequence), but
+ * max_tokens_per_seq may exceed num_tokens.  A sequence
  * whose descriptor is bad (TSD_DEV_BAD_SEQ; here that includes n_b > seq_lens[b]) is skipped: its
  * outputs are not written.
  *

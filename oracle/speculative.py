@@ -85,7 +85,7 @@ class Pool:
     """Page table, lengths and reference counts of a paged cache, and the page contents as labels."""
 
     def __init__(self, table, lens, refs, page, max_len, data=None):
-        self.table, self.lens, self.refs = (np.array(x, np.int64) for x in (table, lens, refs))
+        self.table, self.lens, self.refs = (np.array(np.asarray(x), np.int64) for x in (table, lens, refs))
         self.page, self.max_len = page, max_len
         self.data = None if data is None else data.copy()   # [..., pages at axis 0]
         self.flags = set()

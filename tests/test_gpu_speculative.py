@@ -72,10 +72,11 @@ def make_cache(lens, hkv, page, seed=0, fill="randn", max_len=None, spare=3):
     return cache, table
 
 
-def rows_of(cache, table, b, n, page):
-    """(K, V) of the first n tokens of sequence b as [Hkv, n, 128] float64."""
+def rows_of(cache, table, b, n, page, arrays=None):
+    """(K, V) of the first n tokens of sequence b as [Hkv, n, 128] float64 (arrays: K and V, where they are
+    at hand)."""
     i = np.arange(n)
-    k, v = np64(cache.k), np64(cache.v)
+    k, v = arrays or (np64(cache.k), np64(cache.v))
     if not page:
         return k[b][:, :n], v[b][:, :n]
     p, s = table[b, i // page], i % page
@@ -262,14 +263,14 @@ def test_tree_mask_bad_parents():
 # ---------------------------------------------------------------------------------------------------------------------
 # tree_decode
 # ---------------------------------------------------------------------------------------------------------------------
-def check_tree(cache, table, page, q, counts, lens, rows, out, lse, scale, single=True):
+def check_tree(cache, table, page, q, counts, lens, rows, out, lse, scale):
     hkv, hq = cache.num_kv_heads, q.shape[1]
     G = hq // hkv
     o, l, qq = np64(out), np64(lse), np64(q)
     bf16_out = str(out.dtype) == "torch.bfloat16"
-    t = 0
+    t, arrays = 0, (np64(cache.k), np64(cache.v))
     for b, n in enumerate(counts):
-        K, V = rows_of(cache, table, b, lens[b], page)
+        K, V = rows_of(cache, table, b, lens[b], page, arrays)
         for g in range(hkv):
             ref, rl, spread = S.tree_attention(qq[t:t + n, g * G:(g + 1) * G], K[g], V[g], lens[b] - n, rows[b], scale)
             got, gl = o[t:t + n, g * G:(g + 1) * G], l[t:t + n, g * G:(g + 1) * G]
@@ -345,7 +346,9 @@ def test_tree_one_token_each_and_long():
     run_tree([6, 2], [9000, 20], 8, 2, 16, seed=5)
     run_tree([40, 2], [5000, 3333], 32, 4, 16, seed=6)
     run_tree([3, 4], [10, 20], 4, 2, 16, max_n=7)   # a bound above every count
-    run_tree([1] * 300, [11] * 300, 4, 2, 16, seed=7)   # more sequences than one step of a scan takes
+    run_tree([1] * 300, [11] * 300, 4, 2, 16, seed=7)
+    run_tree(([1] * 3 + [0]) * 350, list(range(40)) * 35, 2, 2, 4, seed=8)   # more sequences than one step of a scan takes
+    run_tree([2, 1], [70, 3], 8, 2, 16, max_n=64)   # a bound above all tokens of the step
 
 
 def test_tree_large_scores():
@@ -432,6 +435,38 @@ def test_tree_tokens_of_no_sequence_are_left_as_they_were():
     tsd.tree_decode(cache, tsd.Queries(q, q_indptr=i32([2, 6, 9]), max_tokens_per_seq=4), None, out=out, lse=lse)
     for x in (out, lse):
         assert (x[:2] == 9).all() and (x[9:] == 9).all() and (x[2:9] != 9).any()
+
+
+def test_a_step_without_tokens():
+    import torch
+    cache, _ = make_cache([40, 30], 2, 16, fill="other")
+    before = cache.k.clone()
+    ip = i32([0, 0, 0])
+    x = torch.zeros(0, 4, 128, device="cuda")
+    mask, depth = tsd.tree_mask(i32(np.zeros(0)), ip, 40)
+    assert mask.shape == (0, 2) and depth.shape == (0,)
+    q = tsd.rope_append(cache, tsd.RotaryEmbedding(), x, x[:, :2], x[:, :2], ip, 40, depth=depth)
+    out, lse = tsd.tree_decode(cache, tsd.Queries(q, ip, 40), mask)
+    assert out.shape == (0, 4, 128) and lse.shape == (0, 4)
+    # and one in which a single sequence has some
+    ip = i32([0, 0, 3])
+    x = torch.randn(3, 4, 128, device="cuda").bfloat16()
+    mask, depth = tsd.tree_mask(i32([-1, 0, 1]), ip, 40)
+    q = tsd.rope_append(cache, tsd.RotaryEmbedding(), x, x[:, :2], x[:, :2], ip, 40, depth=depth)
+    out, lse = tsd.tree_decode(cache, tsd.Queries(q, ip, 40), mask)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all() and not torch.equal(before, cache.k)
+
+
+def test_a_table_of_lengths_that_is_too_long_is_refused_on_the_host():
+    import torch
+    cache, _ = make_cache([40, 30], 2, 16)
+    q = torch.zeros(6, 4, 128, device="cuda")
+    with pytest.raises(ValueError):   # q_indptr of three sequences
+        tsd.tree_decode(cache, tsd.Queries(q, q_indptr=i32([0, 2, 4, 6]), max_tokens_per_seq=3))
+    with pytest.raises(ValueError):
+        tsd.rope_append(cache, tsd.RotaryEmbedding(), q, q[:, :2], q[:, :2], i32([0, 2, 4, 6]), 3)
+    with pytest.raises(ValueError):
+        tsd.cache_compact(cache, i32([[0], [0]]), i32([0, 2, 4, 6]), 3)
 
 
 def test_tree_refusals():

@@ -15,7 +15,15 @@ bool is_pow2(int x);
 // Host validation of the descriptors; fills the kernel views and shape summary.
 tsd_status check_inputs(const tsd_kv_cache* c, const tsd_queries* q, KvView* kv, QView* qv, Shapes* sh);
 
-// The same on shapes alone: device pointers may be NULL.
+// The queries with max_tokens_per_seq held to num_tokens: a loop may keep one bound for steps that
+// draft fewer tokens in all.
+inline tsd_queries bound_tokens(const tsd_queries& queries) {
+  tsd_queries q = queries;
+  if (q.q_indptr != nullptr && q.max_tokens_per_seq > q.num_tokens) q.max_tokens_per_seq = q.num_tokens;
+  return q;
+}
+
+// check_inputs on shapes alone: device pointers may be NULL.
 tsd_status sizes_for(const tsd_kv_cache* cache, const tsd_queries* queries, Shapes* sh);
 
 // The cache descriptor alone.

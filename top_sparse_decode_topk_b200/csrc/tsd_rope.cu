@@ -265,7 +265,9 @@ tsd_status tsd_rope_append(const tsd_kv_cache* cache, const tsd_queries* queries
   RopeArgs a;
   memset(&a, 0, sizeof(a));
   Shapes sh;
-  const tsd_status st = check_inputs(cache, queries, &a.kv, &a.qv, &sh);
+  if (queries == nullptr) return TSD_ERR_INVALID_ARGUMENT;
+  const tsd_queries q = bound_tokens(*queries);
+  const tsd_status st = check_inputs(cache, &q, &a.kv, &a.qv, &sh);
   if (st != TSD_OK) return st;
   if (rope == nullptr || k_new == nullptr || v_new == nullptr || out_q == nullptr) return TSD_ERR_INVALID_ARGUMENT;
   if (rope->rotary_dim < 2 || rope->rotary_dim > 128 || (rope->rotary_dim & 1)) return TSD_ERR_UNSUPPORTED;

@@ -213,6 +213,10 @@ struct TreeWalk {
     left = share;
     if (left <= 0) return;
     s = tree_seq<SH>(a, b, G, false);
+    if (s.tiles == 0 || s.mtiles == 0) {   // only when lengths change under the call
+      left = 0;
+      return;
+    }
     const int unit = off / s.tiles;
     g = unit / s.mtiles;
     mt = unit % s.mtiles;
@@ -230,8 +234,13 @@ struct TreeWalk {
       if (++g == a.kv.hkv) {
         g = 0;
 #pragma unroll 1
-        do s = tree_seq<SH>(a, ++b, G, false);
-        while (s.tiles == 0 || s.mtiles == 0);
+        do {
+          if (++b >= a.kv.batch) {
+            left = 0;
+            return;
+          }
+          s = tree_seq<SH>(a, b, G, false);
+        } while (s.tiles == 0 || s.mtiles == 0);
       }
     }
     cut();
@@ -528,6 +537,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       mbar_init(&ctl->drain[s], 1);
     }
     ctl->abort = 0;
+    ctl->b0 = ctl->off = 0;
     mbar_fence_init();
   }
   if (warp == 10) {
@@ -1215,7 +1225,9 @@ tsd_status tsd_tree_mask(int32_t batch, const int32_t* q_indptr, int32_t num_tok
 
 size_t tsd_tree_decode_workspace_size(const tsd_kv_cache* cache, const tsd_queries* queries, int32_t out_dtype) {
   Shapes sh;
-  if (sizes_for(cache, queries, &sh) != TSD_OK || sh.max_tokens > kMaxTree) return 0;
+  if (queries == nullptr || queries->max_tokens_per_seq > kMaxTree) return 0;
+  const tsd_queries q = bound_tokens(*queries);
+  if (sizes_for(cache, &q, &sh) != TSD_OK) return 0;
   if (out_dtype != TSD_BF16 && out_dtype != TSD_F32) return 0;
   return tree_layout(sh, current_sm_count(), queries->q_dtype == TSD_F32, out_dtype == TSD_F32).total;
 }
@@ -1226,12 +1238,15 @@ tsd_status tsd_tree_decode(const tsd_kv_cache* cache, const tsd_queries* queries
   TreeArgs a;
   Shapes sh;
   memset(&a, 0, sizeof(a));
-  tsd_status st = check_inputs(cache, queries, &a.kv, &a.qv, &sh);
+  if (queries == nullptr) return TSD_ERR_INVALID_ARGUMENT;
+  const tsd_queries q = bound_tokens(*queries);
+  tsd_status st = check_inputs(cache, &q, &a.kv, &a.qv, &sh);
   if (st != TSD_OK) return st;
   if (out == nullptr || ws == nullptr || !queries->causal) return TSD_ERR_INVALID_ARGUMENT;
   if (((uintptr_t)out & 15) || ((uintptr_t)ws & 255)) return TSD_ERR_INVALID_ARGUMENT;
   if (out_dtype != TSD_BF16 && out_dtype != TSD_F32) return TSD_ERR_UNSUPPORTED;
-  if (sh.max_tokens > kMaxTree) return TSD_ERR_UNSUPPORTED;
+  const int max_tokens = queries->q_indptr == nullptr ? 1 : queries->max_tokens_per_seq;
+  if (max_tokens > kMaxTree) return TSD_ERR_UNSUPPORTED;
   a.ctas = current_sm_count();
   const TreeLayout l = tree_layout(sh, a.ctas, a.qv.q_f32, out_dtype == TSD_F32);
   if (ws_bytes < l.total) return TSD_ERR_WORKSPACE_TOO_SMALL;
@@ -1239,7 +1254,7 @@ tsd_status tsd_tree_decode(const tsd_kv_cache* cache, const tsd_queries* queries
   // the line of tiles and the merge's grid are counted in 32 bits
   if ((double)sh.batch * sh.hkv * groups * ((double)sh.max_seq_len / 32 + 8) >= 2147483647.0) return TSD_ERR_UNSUPPORTED;
   a.mask = mask;
-  a.words = (int)(sh.max_tokens + 31) / 32;
+  a.words = (max_tokens + 31) / 32;
   a.part_rows = l.part_rows;
   a.out = out;
   a.out_f32 = out_dtype == TSD_F32;

@@ -10,7 +10,7 @@
     cache_resize(caches, refs, new_lens)               # the rejected drafts' pages go back
     cache_fork(caches, refs, src, dst)                 # sequences that share src's pages
 
-All tensors are on the cache's device.  Nothing here waits for the device, so every call can be
+A step without new tokens (T = 0) is allowed and does nothing.  All tensors are on the cache's device.  Nothing here waits for the device, so every call can be
 captured into a CUDA graph (call it once before, so that the status word below exists).
 
 Outputs and scratch are allocated per call on the call's stream unless the caller passes them, so
@@ -194,6 +194,8 @@ def rope_append(cache: KVCache, rope: RotaryEmbedding, q, k, v, q_indptr=None, m
         out_q = torch.empty((T, Hq, 128), dtype=dtype, device=dev)
     elif out_q.shape != q.shape or out_q.dtype is not dtype or out_q.device != dev or not out_q.is_contiguous():
         raise ValueError("out_q must be a contiguous tensor of q's shape and type")
+    if T == 0:
+        return out_q
     st = _LIB.tsd_rope_append(cs, c, rope.c, q_stride, kp, k_stride, vp, v_stride,
                               None if positions is None else _int32(positions, "positions", dev, (T,)),
                               None if depth is None else _int32(depth, "depth", dev, (T,)), out_q.data_ptr(),
@@ -223,6 +225,8 @@ def tree_mask(parents, q_indptr=None, max_tokens_per_seq: int = 1, mask=None, de
         mask = torch.empty((T, W), dtype=torch.int32, device=dev)
     if depth is None:
         depth = torch.empty((T,), dtype=torch.int32, device=dev)
+    if T == 0:
+        return mask, depth
     st = _LIB.tsd_tree_mask(batch, ip, T, n, pp, _int32(mask, "mask", dev, (T, W)), _int32(depth, "depth", dev, (T,)),
                             _status_ptr(status, dev), _raw_stream(dev))
     if st:
@@ -267,6 +271,8 @@ def tree_decode(cache: KVCache, queries: Queries, mask=None, out=None, out_dtype
         lse = None
     elif lse.shape != (T, Hq) or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 [T, Hq] tensor on the cache's device")
+    if T == 0:
+        return out, lse
     nbytes = _LIB.tsd_tree_decode_workspace_size(cs, qs, code)
     ws, keep, sp = _scratch(workspace, nbytes, "tree_decode", dev, status)
     st = _LIB.tsd_tree_decode(cs, qs, mp, out.data_ptr(), code, None if lse is None else lse.data_ptr(), ws, nbytes, sp,
