@@ -89,7 +89,10 @@ __global__ void __launch_bounds__(kTmThreads) tree_mask_kernel(TreeMaskArgs a) {
 // The rows of a tile are lists: (draft, q head) pairs of one (sequence, kv head), list L = draft * G +
 // head.  With R lists a tile, K and V are read once for all of them and every 512-byte K/V row costs
 // 512 R flop, against a ridge of about 250 flop per byte: up to some 250 lists the cache's bytes bound
-// the kernel, beyond them the tensor cores and the exponentials do.
+// the kernel, beyond them the tensor cores and the exponentials do.  Measured (bf16): 8 contexts of up
+// to 32768 tokens, 16 drafts x 4 heads, 173 us = 6.2 TB/s, 95% of a plain copy's rate; one draft, 170 us;
+// 4 contexts of up to 131072, 32 drafts x 8 heads, 543 us = 1.01 PFLOP/s, 62% of a large library product.
+// There the chain maximum -> exponentials -> P -> products of each stream is what bounds it.
 //
 // Work: unit = (sequence, kv head, tile of kRows lists), cut along the context into tiles of TT tokens.
 // All units' tiles form one line, of which every CTA (one per SM) takes an equal share, so a ragged
@@ -99,7 +102,8 @@ __global__ void __launch_bounds__(kTmThreads) tree_mask_kernel(TreeMaskArgs a) {
 // order of the shares.
 //
 // A CTA: warps 0-3 and 4-7 are two streams of 128 lists, one list a thread (= a tensor-memory lane);
-// warps 8 and 9 issue a stream's MMAs; warps 10 and 11 load the K and V tiles by TMA.
+// warps 8 and 9 issue a stream's MMAs; warps 10 and 12 load the K tiles by TMA, 11 and 13 the V tiles,
+// every other tile each (one warp issues a box in some 80 cycles, too slow for pages of 16).
 //   S_s = Q_s K^T   (M 128, N TT, K 128; operands in shared memory, fp32 in tensor memory)
 //   softmax in registers: running maximum and sum per thread, P rounded to bf16 into tensor memory
 //   O_s += P_s V    (M 128, N 128, K TT; P from tensor memory, V MN-major from shared memory)
@@ -107,11 +111,14 @@ __global__ void __launch_bounds__(kTmThreads) tree_mask_kernel(TreeMaskArgs a) {
 // streams hold different lists and share each K and V tile.  Up to 128 (DUAL false): both hold the
 // same lists and take alternate tiles; their states are merged at the segment's end.
 // O is rescaled lazily: only when a maximum grows by more than 2^8, so weights stay below 2^8.
+// With different lists, a warp of each stream shares an SM quarter's exponential unit: they take it in
+// turn, so that one's exponentials run under the other's waits (128K case: 576 us without).
 //
 // Precision: fp32 queries enter as three bf16 parts (QP = 3, exact to 2^-24); with fp32 outputs the
-// weights do too (PP = 3), over tiles of 64 tokens so that the parts fit the tensor memory that S
-// leaves free.  With bf16 outputs the weights are rounded to bf16 once (2^-8 at most, averaged over
-// the row), as the outputs are; the sum l is always of the unrounded fp32 weights.
+// weights do too (PP = 3).  With bf16 outputs the weights are rounded to bf16 once (2^-8 at most,
+// averaged over the row), as the outputs are; the sum l is always of the unrounded fp32 weights.
+// The 64-list case above: fp32 queries 227 us (three times the score products), fp32 outputs 287 us,
+// both 350 us: there the tensor cores' floor is some 180 us and the longer softmax chain the rest.
 //
 // Tiles that reach past the committed tokens ("special": drafts, or the end of the sequence) take a
 // longer path: scores are masked by each list's bits; rows of V behind the sequence are zeroed in
@@ -138,14 +145,22 @@ struct TreeArgs {
 };
 
 constexpr int kTaThreads = 512;
-constexpr int kTaSoftmaxRegs = 168, kTaOtherRegs = 88;
+// 8 warps x 32 x (192 + 64) = the 65536 registers of 512 threads at 128.  A softmax thread holds a row
+// of 64 scores; the other roles need no more than 64.
+constexpr int kTaSoftmaxRegs = 192, kTaOtherRegs = 64;
 constexpr int kTaRowsPerStream = 128;
 constexpr int kTaTiles = 229376;               // Q tiles and the ring
 constexpr size_t kTaSmem = kTaTiles + 3072;    // then barriers and scratch: all of an SM's shared memory
 
 template <int QP, int PP>
 struct TreeShape {
-  static constexpr int TT = PP == 1 ? 64 : 32;               // tokens of a tile
+  // Weights in three parts (PP = 3) take 1.5 tensor-memory columns a token, and a stream has 128 columns
+  // for S and P.  fp32 queries: tiles of 64 tokens, P in two halves of 32 behind S (kSplit), which keeps
+  // the scores' three parts at N 64.  bf16 queries: tiles of 32 tokens, whose S and P are double-buffered.
+  // Measured (8 x 32K context, 64 lists), split and not: fp32 queries 344 and 387 us, bf16 310 and 287.
+  static constexpr bool kSplit = QP == 3 && PP == 3;
+  static constexpr int TT = PP == 1 || kSplit ? 64 : 32;     // tokens of a tile
+  static constexpr int PT = kSplit ? 32 : TT;                // tokens whose weights P holds at a time
   static constexpr int kRows = QP == 1 ? 256 : 128;          // lists of a unit: two Q tiles, or one in three parts
   static constexpr int kQBytes = (QP == 1 ? 2 : 3) * 32768;
   static constexpr int kSlotBytes = TT * 256;                // one K or V tile
@@ -159,7 +174,7 @@ struct TreeShape {
   // Steps whose products add up in tensor memory before they are moved to fp32 sums in global
   // memory (fp32 outputs only; 0: never).  The tensor cores truncate each sum: measured, V = 1 came out
   // 6.6e-9 low per accumulation, 2e-5 over 80000 tokens.
-  static constexpr int kFlush = PP == 1 ? 0 : 16;
+  static constexpr int kFlush = PP == 1 ? 0 : 512 / TT;
 };
 
 // What one sequence contributes: its descriptor and its units.
@@ -255,9 +270,11 @@ struct TreeWalk {
 // Shared-memory control block behind the Q tiles and the ring.
 struct TreeCtl {
   uint64_t k_full[8], k_empty[8], v_full[12], v_empty[12];
-  // [stream][buffer of S and P]: step k of a stream uses buffer k % 2 and these barriers' phase k / 2.
-  // s_full of step k implies that the products of step k - 2 are done, so no wait is two phases behind.
-  uint64_t q_ready, s_full[2][2], p_ready[2][2], o_done[2][2], fixed[2], drain[2];
+  // A stream's 128 columns for S and P are two buffers: step k keeps both in buffer k % 2, with these
+  // barriers' phase k / 2; s_full of step k implies that the products of step k - 2 are done, so no wait
+  // is two phases behind.  Split: S has columns 0 to 63, free again (s_free) as soon as the softmax has
+  // read it, P those behind it; p_ready[s][0] and o_done[s][0] count halves of steps.
+  uint64_t q_ready, s_full[2][2], s_free[2], p_ready[2][2], o_done[2][2], fixed[2], drain[2];
   uint32_t abort, tmem, nf[2][2];
   // Rows with a bad page of tile m (counted over the CTA's share), at m % 32: K is loaded at most
   // 4 (two steps of two streams) + kKSlots <= 12 tiles ahead of the softmax.
@@ -281,10 +298,23 @@ __device__ __forceinline__ void tree_wait(uint64_t* bar, uint32_t parity, TreeCt
     }
   }
 }
-// The same by all lanes of a warp, converged again behind it (as .aligned instructions need).
+// Whether the phase of the given parity is complete.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+
+// tree_wait by all lanes of a warp, converged again behind it (as .aligned instructions need).  Most
+// phases are complete by the time they are waited for, and a test says so sooner than a try.
 __device__ __forceinline__ void tree_wait_warp(uint64_t* bar, uint32_t parity, TreeCtl* c, uint32_t* status) {
-  tree_wait(bar, parity, c, status);
-  __syncwarp();
+  if (!__all_sync(0xFFFFFFFFu, mbar_test(bar, parity))) {
+    tree_wait(bar, parity, c, status);
+    __syncwarp();
+  }
 }
 
 template <int N>
@@ -294,16 +324,6 @@ __device__ __forceinline__ void take_registers() {
 template <int N>
 __device__ __forceinline__ void give_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-
-// Whether the phase of the given parity is complete.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-               : "=r"(ok)
-               : "r"(smem_u32(bar)), "r"(parity)
-               : "memory");
-  return ok != 0;
 }
 
 // One lane of a converged warp.
@@ -459,8 +479,8 @@ __device__ __noinline__ uint64_t tree_clean_v(unsigned char* vt, uint32_t* found
 }
 
 // Adds to O the products of the rows of V that were zeroed for their infinities or NaNs (`rows`), for
-// the lists that see them (`seen`).  The tile's P is still in tensor memory, at tp.
-template <int TT, int PP>
+// the lists that see them (`seen`).  P, of PT tokens, is still in tensor memory, at tp.
+template <int PT, int PP>
 __device__ __noinline__ void tree_add_nonfinite(const KvView& kv, int b, int g, int t0, uint64_t rows, uint64_t seen,
                                                 uint32_t tp, uint32_t to) {
   for (; rows != 0; rows &= rows - 1) {
@@ -468,7 +488,7 @@ __device__ __noinline__ void tree_add_nonfinite(const KvView& kv, int b, int g, 
     float p = 0.f;
 #pragma unroll 1
     for (int part = 0; part < PP; ++part) {
-      uint32_t w = tmem_ld1(tp + part * (TT / 2) + (r >> 1));
+      uint32_t w = tmem_ld1(tp + part * (PT / 2) + ((r % PT) >> 1));
       tmem_wait_ld();
       asm volatile("" : "+r"(w));
       p += (r & 1) ? bf16hi(w) : bf16lo(w);
@@ -533,6 +553,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         mbar_init(&ctl->p_ready[s][d], 128);
         mbar_init(&ctl->o_done[s][d], 1);
       }
+      mbar_init(&ctl->s_free[s], 128);
       mbar_init(&ctl->fixed[s], 128);
       mbar_init(&ctl->drain[s], 1);
     }
@@ -617,7 +638,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       const int list = first + row;
       const bool valid = list < lists, warp_live = first + 32 * (warp & 3) < lists;
       // the warp of the other stream on the same quarter of the SM has work too
-      const bool pair = dual && wk.mt * SH::kRows + kTaRowsPerStream + 32 * (warp & 3) < lists;
+      const bool pair = PP == 1 && dual && wk.mt * SH::kRows + kTaRowsPerStream + 32 * (warp & 3) < lists;
       if (pair && s == 1) pair_arrive(4 + 2 * (warp & 3));   // stream 0 goes first
       const int j = list / G, h = wk.g * G + (list - j * G);
       named_sync(1, 256);   // the previous segment's Q tiles and states are done with
@@ -664,30 +685,42 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       float m = -INFINITY, l = 0.f;
       float m_sum = -INFINITY;   // reference of the sums moved to global memory; -inf: none yet
       uint64_t seen = 0;         // the special tile's tokens that this list sees
+      auto products_done = [&](uint32_t step) {   // O holds all products up to this step's
+        if (!SH::kSplit) tree_wait_warp(&ctl->o_done[s][step & 1], (step >> 1) & 1, ctl, a.status);
+        else tree_wait_warp(&ctl->o_done[s][0], 1, ctl, a.status);   // its second half
+        tc_fence_after_sync();
+      };
 #pragma unroll 1
       for (int i = 0; i < steps; ++i) {
         const int at = dual ? i : 2 * i + s, tile = wk.k0 + at;
         const uint32_t step = done + i, num = tiles_done + at;
         const bool special = (tile + 1) * TT > sq.base;
-        const uint32_t tp = tm + (step & 1) * 64;
+        const uint32_t buf = SH::kSplit ? 0 : step & 1, tb = tm + buf * 64;   // S
         if (SH::kFlush && i > 0 && i % (SH::kFlush ? SH::kFlush : 1) == 0 && warp_live) {
-          tree_wait_warp(&ctl->o_done[s][(step - 1) & 1], ((step - 1) >> 1) & 1, ctl, a.status);
-          tc_fence_after_sync();
+          products_done(step - 1);
           tree_flush(to, sums, m_sum == -INFINITY ? 0.f : fast_exp2(m_sum - m), m_sum != -INFINITY, valid);
           m_sum = m;
         }
-        if (!__all_sync(0xFFFFFFFFu, mbar_test(&ctl->s_full[s][step & 1], (step >> 1) & 1)))
-          tree_wait_warp(&ctl->s_full[s][step & 1], (step >> 1) & 1, ctl, a.status);
+        const uint32_t s_phase = (SH::kSplit ? step : step >> 1) & 1;
+        tree_wait_warp(&ctl->s_full[s][buf], s_phase, ctl, a.status);
         tc_fence_after_sync();
+        float x[TT];
+        uint32_t bad0 = 0, bad1 = 0;
         if (warp_live) {
-          float x[TT];
 #pragma unroll
-          for (int c = 0; c < TT / 32; ++c) tmem_ld32(tp + 32 * c, x + 32 * c);
+          for (int c = 0; c < TT / 32; ++c) tmem_ld32(tb + 32 * c, x + 32 * c);
           const volatile uint32_t* marks = ctl->bad[num & 31];
-          const uint32_t bad0 = marks[0], bad1 = TT > 32 ? marks[1] : 0;
+          bad0 = marks[0];
+          if (TT > 32) bad1 = marks[1];
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < TT / 32; ++c) tmem_loaded32(x + 32 * c);
+        }
+        if (SH::kSplit) {
+          tc_fence_before_sync();
+          mbar_arrive(&ctl->s_free[s]);
+        }
+        if (warp_live) {
           if (special || (bad0 | bad1)) {
             const uint64_t bad = (uint64_t)bad1 << 32 | bad0;
             seen = valid ? tree_visible<TT>(a, sq, j, tile * TT) & ~bad : 0u;
@@ -708,68 +741,100 @@ __global__ void __launch_bounds__(kTaThreads, 1)
               const float f = grow ? fast_exp2(m - mx) : 1.f;
               if (grow) m = mx;
               l *= f;
-              tree_wait_warp(&ctl->o_done[s][(step - 1) & 1], ((step - 1) >> 1) & 1, ctl, a.status);
-              tc_fence_after_sync();
+              products_done(step - 1);
               tree_scale(to, f);
             }
           }
-          const float ref = m == -INFINITY ? 0.f : m;   // nothing seen yet: weights 0
-          if (pair) pair_wait(4 + 2 * (warp & 3) + s);
-          const float2 scale2 = make_float2(scale, scale), ref2 = make_float2(-ref, -ref);
-          float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int c = 0; c < TT / 32; ++c) {
-            float* p = x + 32 * c;
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 z = __ffma2_rn(make_float2(p[e], p[e + 1]), scale2, ref2);
-              p[e] = fast_exp2(z.x);
-              p[e + 1] = fast_exp2(z.y);
-              l2[(e >> 1) & 1] = __fadd2_rn(l2[(e >> 1) & 1], make_float2(p[e], p[e + 1]));
-            }
-#pragma unroll
-            for (int part = 0; part < PP; ++part) {
-              uint32_t w[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                w[e] = cvt_bf16x2(p[2 * e], p[2 * e + 1]);
-                if (part + 1 < PP) {
-                  p[2 * e] -= bf16lo(w[e]);
-                  p[2 * e + 1] -= bf16hi(w[e]);
-                }
-              }
-              tmem_st16(tp + part * (TT / 2) + 16 * c, w);
-            }
-          }
-          if (pair) pair_arrive(4 + 2 * (warp & 3) + (s ^ 1));
-          l2[0] = __fadd2_rn(l2[0], l2[1]);
-          l += l2[0].x + l2[0].y;
-          tmem_wait_st();
         }
+        const float ref = m == -INFINITY ? 0.f : m;   // nothing seen yet: weights 0
+        const float2 scale2 = make_float2(scale, scale), ref2 = make_float2(-ref, -ref);
         uint64_t odd = 0;
-        if (special) {
+        auto clean_v = [&]() {
           const uint32_t slot = num % VS;
           tree_wait_warp(&ctl->v_full[slot], (num / VS) & 1, ctl, a.status);
           odd = tree_clean_v<TT>(vring + (size_t)slot * SH::kSlotBytes, ctl->nf[dual ? 0 : s], tile * TT, sq.base, sq.len,
                                  dual ? tid : row, dual ? 256 : 128, dual ? 1 : 2 + s);
-        }
-        tc_fence_before_sync();
-        mbar_arrive(&ctl->p_ready[s][step & 1]);
-        if (special) {
-          if (odd != 0 && warp_live) {
-            tree_wait_warp(&ctl->o_done[s][step & 1], (step >> 1) & 1, ctl, a.status);
-            tc_fence_after_sync();
-            tree_add_nonfinite<TT, PP>(a.kv, wk.b, wk.g, tile * TT, odd, seen, tp, to);
-            tc_fence_before_sync();
+        };
+        // Weights of 32 tokens: exponentials and their sum, then P in PP parts.
+        float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        auto weigh = [&](float* p) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 z = __ffma2_rn(make_float2(p[e], p[e + 1]), scale2, ref2);
+            p[e] = fast_exp2(z.x);
+            p[e + 1] = fast_exp2(z.y);
+            l2[(e >> 1) & 1] = __fadd2_rn(l2[(e >> 1) & 1], make_float2(p[e], p[e + 1]));
           }
-          if (i + 2 < steps) mbar_arrive(&ctl->fixed[s]);
+        };
+        auto store_p = [&](float* p, uint32_t at) {
+#pragma unroll
+          for (int part = 0; part < PP; ++part) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              w[e] = cvt_bf16x2(p[2 * e], p[2 * e + 1]);
+              if (part + 1 < PP) {
+                p[2 * e] -= bf16lo(w[e]);
+                p[2 * e + 1] -= bf16hi(w[e]);
+              }
+            }
+            tmem_st16(at + part * (SH::PT / 2), w);
+          }
+        };
+        if constexpr (!SH::kSplit) {
+          if (warp_live) {
+            if (pair) pair_wait(4 + 2 * (warp & 3) + s);
+#pragma unroll
+            for (int c = 0; c < TT / 32; ++c) {
+              weigh(x + 32 * c);
+              store_p(x + 32 * c, tb + 16 * c);
+            }
+            if (pair) pair_arrive(4 + 2 * (warp & 3) + (s ^ 1));
+            l2[0] = __fadd2_rn(l2[0], l2[1]);
+            l += l2[0].x + l2[0].y;
+            tmem_wait_st();
+          }
+          if (special) clean_v();
+          tc_fence_before_sync();
+          mbar_arrive(&ctl->p_ready[s][buf]);
+          if (special) {
+            if (odd != 0 && warp_live) {
+              products_done(step);
+              tree_add_nonfinite<SH::PT, PP>(a.kv, wk.b, wk.g, tile * TT, odd, seen, tb, to);
+              tc_fence_before_sync();
+            }
+            if (i + 2 < steps) mbar_arrive(&ctl->fixed[s]);
+          }
+        } else {
+          if (special) clean_v();
+          const uint32_t tp = tm + 64;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (warp_live) weigh(x + 32 * c);
+            // the products of the half before this one
+            if (c > 0 || step > 0) tree_wait_warp(&ctl->o_done[s][0], c ^ 1, ctl, a.status);
+            if (warp_live) {
+              store_p(x + 32 * c, tp);
+              tmem_wait_st();
+            }
+            tc_fence_before_sync();
+            mbar_arrive(&ctl->p_ready[s][0]);
+            if (special) {
+              const uint64_t here = odd & (c ? ~0ull << 32 : 0xFFFFFFFFull);
+              if (here != 0) {
+                tree_wait_warp(&ctl->o_done[s][0], c, ctl, a.status);
+                tc_fence_after_sync();
+                if (warp_live) tree_add_nonfinite<SH::PT, PP>(a.kv, wk.b, wk.g, tile * TT, here, seen, tp, to);
+                tc_fence_before_sync();
+              }
+            }
+          }
+          l2[0] = __fadd2_rn(l2[0], l2[1]);
+          if (warp_live) l += l2[0].x + l2[0].y;
         }
       }
       if (pair && s == 0) pair_wait(4 + 2 * (warp & 3));   // the other stream's last turn
-      if (steps > 0) {
-        const uint32_t last = done + steps - 1;
-        tree_wait_warp(&ctl->o_done[s][last & 1], (last >> 1) & 1, ctl, a.status);
-      }
+      if (steps > 0) products_done(done + steps - 1);
       tc_fence_after_sync();
       done += steps;
       tiles_done += ntile;
@@ -981,12 +1046,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         tree_wait_warp(&ctl->q_ready, segs & 1, ctl, a.status);
         tc_fence_after_sync();
         auto scores = [&](int i) {
-          const uint32_t n = tiles_done + first + stride * i, slot = n % KS, buf = (done + i) & 1;
+          const uint32_t n = tiles_done + first + stride * i, slot = n % KS, buf = SH::kSplit ? 0 : (done + i) & 1;
           tree_wait_warp(&ctl->k_full[slot], (n / KS) & 1, ctl, a.status);
           tc_fence_after_sync();
           if (!elect_one()) return;
           const uint64_t kd = ring_k + (uint64_t)(slot * (SH::kSlotBytes >> 4));
-#pragma unroll
+#pragma unroll 1
           for (int p = QP - 1; p >= 0; --p)   // the small parts first: every step rounds the sum so far
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
@@ -996,36 +1061,69 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           umma_commit(&ctl->k_empty[slot]);   // expects both streams; a tile of one stream counts twice
           if (!dual) umma_commit(&ctl->k_empty[slot]);
         };
+        // O += P V over the P's tokens, from k step k0 of the tile on; the small parts first
+        auto products = [&](uint32_t pt, uint64_t vd, int k0, bool fresh) {
+#pragma unroll
+          for (int p = PP - 1; p >= 0; --p)
+#pragma unroll
+            for (int ks = 0; ks < SH::PT / 16; ++ks)
+              umma_bf16_ts(tm + 128, pt + p * (SH::PT / 2) + ks * 8, vd + ((k0 + ks) * 2048 >> 4), idesc_o,
+                           !fresh || p < PP - 1 || ks > 0);
+        };
+        if constexpr (!SH::kSplit) {
 #pragma unroll 1
-        for (int i = -2; i < steps; ++i) {
-          const int at = first + stride * i;
-          if (i >= 0) {
-            const uint32_t n = tiles_done + at, slot = n % VS, buf = (done + i) & 1;
-            tree_wait_warp(&ctl->v_full[slot], (n / VS) & 1, ctl, a.status);
-            tree_wait_warp(&ctl->p_ready[s][buf], ((done + i) >> 1) & 1, ctl, a.status);
-            tc_fence_after_sync();
-            if (elect_one()) {
-            const uint64_t vd = ring_v + (uint64_t)(slot * (SH::kSlotBytes >> 4));
-            const bool fresh = SH::kFlush ? i % (SH::kFlush ? SH::kFlush : 1) == 0 : i == 0;
-#pragma unroll
-            for (int p = PP - 1; p >= 0; --p)
-#pragma unroll
-              for (int ks = 0; ks < TT / 16; ++ks)
-                umma_bf16_ts(tm + 128, tm + buf * 64 + p * (TT / 2) + ks * 8, vd + (ks * 2048 >> 4), idesc_o,
-                             !fresh || p < PP - 1 || ks > 0);
-            umma_commit(&ctl->o_done[s][buf]);
-            umma_commit(&ctl->v_empty[slot]);
-            if (!dual) umma_commit(&ctl->v_empty[slot]);
-            }
-            __syncwarp();
-          }
-          if (i + 2 < steps) {
-            if (i >= 0 && (wk.k0 + at + 1) * TT > wk.s.base) {   // a special tile: P is read once more
-              tree_wait_warp(&ctl->fixed[s], fixes++ & 1, ctl, a.status);
+          for (int i = -2; i < steps; ++i) {
+            const int at = first + stride * i;
+            if (i >= 0) {
+              const uint32_t n = tiles_done + at, slot = n % VS, buf = (done + i) & 1;
+              tree_wait_warp(&ctl->v_full[slot], (n / VS) & 1, ctl, a.status);
+              tree_wait_warp(&ctl->p_ready[s][buf], ((done + i) >> 1) & 1, ctl, a.status);
               tc_fence_after_sync();
+              if (elect_one()) {
+                products(tm + buf * 64, ring_v + (uint64_t)(slot * (SH::kSlotBytes >> 4)), 0,
+                         SH::kFlush ? i % (SH::kFlush ? SH::kFlush : 1) == 0 : i == 0);
+                umma_commit(&ctl->o_done[s][buf]);
+                umma_commit(&ctl->v_empty[slot]);
+                if (!dual) umma_commit(&ctl->v_empty[slot]);
+              }
+              __syncwarp();
             }
-            scores(i + 2);
-            __syncwarp();
+            if (i + 2 < steps) {
+              if (i >= 0 && (wk.k0 + at + 1) * TT > wk.s.base) {   // a special tile: P is read once more
+                tree_wait_warp(&ctl->fixed[s], fixes++ & 1, ctl, a.status);
+                tc_fence_after_sync();
+              }
+              scores(i + 2);
+              __syncwarp();
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int i = -1; i < steps; ++i) {
+            if (i + 1 < steps) {   // S(i + 1) is made while the weights of S(i) are
+              if (done + i + 1 > 0) tree_wait_warp(&ctl->s_free[s], (done + i) & 1, ctl, a.status);
+              tc_fence_after_sync();
+              scores(i + 1);
+              __syncwarp();
+            }
+            if (i < 0) continue;
+            const uint32_t n = tiles_done + first + stride * i, slot = n % VS;
+            const uint64_t vd = ring_v + (uint64_t)(slot * (SH::kSlotBytes >> 4));
+            tree_wait_warp(&ctl->v_full[slot], (n / VS) & 1, ctl, a.status);
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              tree_wait_warp(&ctl->p_ready[s][0], c, ctl, a.status);
+              tc_fence_after_sync();
+              if (elect_one()) {
+                products(tm + 64, vd, 2 * c, c == 0 && i % (SH::kFlush ? SH::kFlush : 1) == 0);
+                umma_commit(&ctl->o_done[s][0]);
+                if (c == 1) {
+                  umma_commit(&ctl->v_empty[slot]);
+                  if (!dual) umma_commit(&ctl->v_empty[slot]);
+                }
+              }
+              __syncwarp();
+            }
           }
         }
         tiles_done += ntile;
@@ -1266,7 +1364,8 @@ tsd_status tsd_tree_decode(const tsd_kv_cache* cache, const tsd_queries* queries
   a.part_acc = reinterpret_cast<float4*>(w + l.acc);
   a.sums = reinterpret_cast<float4*>(w + l.sums);
   KvMaps maps;
-  st = make_kv_maps(cache, &maps, a.out_f32 ? TreeShape<1, 3>::TT : TreeShape<1, 1>::TT, true);
+  st = make_kv_maps(cache, &maps, a.out_f32 && !a.qv.q_f32 ? TreeShape<1, 3>::TT : TreeShape<3, 3>::TT, true);
+  static_assert(TreeShape<3, 3>::TT == TreeShape<1, 1>::TT && TreeShape<3, 3>::TT == TreeShape<3, 1>::TT, "boxes of a tile");
   if (st != TSD_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
