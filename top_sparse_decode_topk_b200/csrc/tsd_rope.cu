@@ -8,10 +8,11 @@
 // point and no range reduction.
 //
 // Bound by HBM: a token moves (Hq + Hkv) x 256 B in and out and Hkv x 512 B of V (bf16).  One
-// block takes a few tokens of one sequence: its first threads compute the tokens' sines and cosines
+// block takes one or a few tokens of a sequence: its first threads compute the tokens' sines and cosines
 // once (64 per token, shared by all heads), the rest of the work is 16-byte loads and stores.
 // A thread takes two 16-byte chunks of a row that hold both elements of its pairs, so q can be
-// rotated in place.
+// rotated in place.  Measured, 32 + 8 + 8 heads: 32768 tokens 133 us = 6.1 TB/s (93% of a plain
+// copy's rate), 8192 39 us, 64 6.3 us with the launch.
 #include <math.h>
 #include <string.h>
 
@@ -67,7 +68,8 @@ __device__ __forceinline__ void turn_pair(float& a, float& b, const float2 cs) {
 }
 
 // VEC: the rotated dims split into whole 16-byte chunks on both sides of every pair (half layout:
-// rotary_dim a multiple of 16; interleaved: of 8); otherwise element by element.
+// rotary_dim a multiple of 16; interleaved: of 8); otherwise element by element (32768 tokens: 344 us;
+// in the half layout a pair's elements then lie at different places of their chunks).
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float2 cs[kRopeMaxToks][64];
@@ -288,8 +290,9 @@ tsd_status tsd_rope_append(const tsd_kv_cache* cache, const tsd_queries* queries
   a.depth = depth;
   a.out_q = out_q;
   a.status = status;
-  // several tokens a block once every SM has its share of blocks
-  a.toks = sh.tokens >= 4LL * 4 * current_sm_count() ? kRopeMaxToks : 1;
+  // A token a block (four were no faster: 136 us against 133 at 32768 tokens, 47 against 39 at 8192),
+  // unless the bound lies far above most sequences, where most blocks find no token.
+  a.toks = (int64_t)sh.batch * sh.max_tokens > 4LL * sh.tokens ? kRopeMaxToks : 1;
   const int64_t per_seq = (sh.max_tokens + a.toks - 1) / a.toks;
   if (per_seq * sh.batch > 0x7fffffffLL) return TSD_ERR_UNSUPPORTED;
   a.chunks = (int)per_seq;
