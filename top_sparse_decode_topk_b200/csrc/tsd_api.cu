@@ -130,7 +130,7 @@ tsd_status make_kv_maps(const tsd_kv_cache* c, KvMaps* maps, int max_box, bool g
   } else {
     if (c->page_size < 8 && !gather) return TSD_OK;
     rows = c->num_pages * c->num_kv_heads * c->page_size;
-    box_rows = c->page_size < 8 ? 1 : (c->page_size < max_box ? c->page_size : max_box);
+    box_rows = c->page_size < 4 ? 1 : (c->page_size < max_box ? c->page_size : max_box);
   }
   if (rows >= (int64_t)1 << 31) return TSD_ERR_UNSUPPORTED;
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;

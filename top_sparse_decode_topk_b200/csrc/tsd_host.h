@@ -30,9 +30,9 @@ tsd_status sizes_for(const tsd_kv_cache* cache, const tsd_queries* queries, Shap
 tsd_status check_cache_only(const tsd_kv_cache* cache, KvView* kv, Shapes* sh);
 
 // Tensor maps of K and V seen as [rows][128] bf16 with a {64, box} box and 128-byte swizzling,
-// box = min(max_box, page_size) rows (max_box for the contiguous layout).  For pages of less than 8
-// tokens: with `gather`, boxes one row high (tile::gather4 loads), else zeroed maps (their tiles are
-// copied with cp.async).
+// box = min(max_box, page_size) rows (max_box for the contiguous layout).  With `gather`, boxes are one
+// row high for pages of less than 4 tokens (tile::gather4 loads); without it, maps are zeroed for pages
+// of less than 8 (their tiles are copied with cp.async).
 tsd_status make_kv_maps(const tsd_kv_cache* c, KvMaps* maps, int max_box = 16, bool gather = false);
 
 // SM count of the current device (148 when none can be queried).

@@ -927,8 +927,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     unsigned char* ring = is_v ? vring : kring;
     uint64_t *full = is_v ? ctl->v_full : ctl->k_full, *empty = is_v ? ctl->v_empty : ctl->k_empty;
     const uint32_t slots = is_v ? VS : KS;
-    // Pages of 8 or more tokens: boxes of `per` rows, one a lane; smaller pages: four rows a lane.
-    const bool paged = a.kv.page_table != nullptr, gather = paged && a.kv.page_shift < 3;
+    // Pages of 4 or more tokens: boxes of `per` rows, one a lane; smaller pages: four rows a lane.
+    // Measured, 8 x 16 drafts over 32K: pages of 8 178 us in boxes, 280 gathered; of 4 253 and 280; of 1
+    // 282 (a copy instruction for every four rows and half row).
+    const bool paged = a.kv.page_table != nullptr, gather = paged && a.kv.page_shift < 2;
     const int shift = paged ? a.kv.page_shift : 0, in_page = (1 << shift) - 1;
     const int per = !paged ? TT : (gather ? 4 : min(TT, 1 << shift));
     const int per_tile = TT / per, window = 32 / per_tile;   // boxes of a tile, tiles of 32 boxes
