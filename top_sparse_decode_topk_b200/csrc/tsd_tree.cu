@@ -117,8 +117,8 @@ __global__ void __launch_bounds__(kTmThreads) tree_mask_kernel(TreeMaskArgs a) {
 // Precision: fp32 queries enter as three bf16 parts (QP = 3, exact to 2^-24); with fp32 outputs the
 // weights do too (PP = 3).  With bf16 outputs the weights are rounded to bf16 once (2^-8 at most,
 // averaged over the row), as the outputs are; the sum l is always of the unrounded fp32 weights.
-// The 64-list case above: fp32 queries 227 us (three times the score products), fp32 outputs 287 us,
-// both 350 us: there the tensor cores' floor is some 180 us and the longer softmax chain the rest.
+// The 64-list case above: fp32 queries 227 us (three times the score products), fp32 outputs 297 us,
+// both 357 us: there the tensor cores' floor is some 180 us and the longer softmax chain the rest.
 //
 // Tiles that reach past the committed tokens ("special": drafts, or the end of the sequence) take a
 // longer path: scores are masked by each list's bits; rows of V behind the sequence are zeroed in
@@ -157,7 +157,8 @@ struct TreeShape {
   // Weights in three parts (PP = 3) take 1.5 tensor-memory columns a token, and a stream has 128 columns
   // for S and P.  fp32 queries: tiles of 64 tokens, P in two halves of 32 behind S (kSplit), which keeps
   // the scores' three parts at N 64.  bf16 queries: tiles of 32 tokens, whose S and P are double-buffered.
-  // Measured (8 x 32K context, 64 lists), split and not: fp32 queries 344 and 387 us, bf16 310 and 287.
+  // Measured (8 x 32K context, 64 lists), split and not (moving O every
+  // 512 tokens): fp32 queries 344 and 387 us, bf16 310 and 287.
   static constexpr bool kSplit = QP == 3 && PP == 3;
   static constexpr int TT = PP == 1 || kSplit ? 64 : 32;     // tokens of a tile
   static constexpr int PT = kSplit ? 32 : TT;                // tokens whose weights P holds at a time
@@ -173,8 +174,9 @@ struct TreeShape {
   static_assert(kKSlots % 2 == 0 && kVSlots % 2 == 0 && kKSlots >= 4 && kVSlots >= 4, "ring slots");
   // Steps whose products add up in tensor memory before they are moved to fp32 sums in global
   // memory (fp32 outputs only; 0: never).  The tensor cores truncate each sum: measured, V = 1 came out
-  // 6.6e-9 low per accumulation, 2e-5 over 80000 tokens.
-  static constexpr int kFlush = PP == 1 ? 0 : 512 / TT;
+  // 6.6e-9 low per accumulation, 2e-5 over 80000 tokens.  Every 512, 256, 128 tokens: errors up to 1.5,
+  // 1.25, 0.85 of a plain fp32 form's; 64 bf16 lists over 8 x 32K in 278, 297, 341 us.
+  static constexpr int kFlush = PP == 1 ? 0 : 256 / TT;
 };
 
 // What one sequence contributes: its descriptor and its units.
@@ -392,7 +394,13 @@ __device__ __noinline__ void tree_scale(uint32_t to, float f) {
   tmem_wait_st();
 }
 
-// sums = sums * f + O (sums are taken as 0 when !have): this list's column of [32][128] float4.
+// Four floats are added to *p in L2 (by this thread alone, so in a fixed order).
+__device__ __forceinline__ void red_add4(float4* p, const float* x) {
+  asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]) : "memory");
+}
+
+// sums = sums * f + O (sums are taken as 0 when !have): this list's column of [32][128] float4.  Added
+// in L2, without a wait, when f is 1.
 __device__ __noinline__ void tree_flush(uint32_t to, float4* sums, float f, bool have, bool valid) {
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
@@ -405,9 +413,13 @@ __device__ __noinline__ void tree_flush(uint32_t to, float4* sums, float f, bool
 #pragma unroll
     for (int d = 0; d < 8; ++d) {
       float4* p = sums + (8 * c + d) * kTaRowsPerStream;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (have) x = __ldcg(p);
-      __stcg(p, make_float4(x.x * f + o[4 * d], x.y * f + o[4 * d + 1], x.z * f + o[4 * d + 2], x.w * f + o[4 * d + 3]));
+      if (have && f == 1.f) {
+        red_add4(p, o + 4 * d);
+      } else {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (have) x = __ldcg(p);
+        __stcg(p, make_float4(x.x * f + o[4 * d], x.y * f + o[4 * d + 1], x.z * f + o[4 * d + 2], x.w * f + o[4 * d + 3]));
+      }
     }
   }
 }
