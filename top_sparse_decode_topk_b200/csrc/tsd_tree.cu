@@ -395,7 +395,7 @@ __device__ __noinline__ void tree_scale(uint32_t to, float f) {
   tmem_wait_st();
 }
 
-// Four floats are added to *p in L2 (by this thread alone, so in a fixed order).
+// Four floats are added to *p in L2 (by this thread alone, so in a fixed order; subnormal sums count as 0).
 __device__ __forceinline__ void red_add4(float4* p, const float* x) {
   asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]) : "memory");
 }
