@@ -400,6 +400,54 @@ def test_tree_masked_drafts_may_hold_anything(what, ot):
             assert torch.equal(lse[sees], rl[sees])
 
 
+@pytest.mark.parametrize("qt", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [5, 70])
+def test_tree_sums_over_long_contexts(qt, n):
+    """fp32 outputs over contexts long enough that sums leave tensor memory several times, with scores that grow along
+    the context, so that what was summed is rescaled afterwards."""
+    import torch
+    counts, before, hq, hkv, page = [n, 3], [24990, 20], 16, 8, 16
+    lens = [a + c for a, c in zip(before, counts)]
+    cache, table = make_cache(lens, hkv, page, 9)
+    for b, length in enumerate(lens):
+        i = np.arange(length)
+        ramp = torch.from_numpy(0.1 + 3.0 * i / length).cuda().to(torch.bfloat16)
+        at = torch.from_numpy(table[b, i // page].astype(np.int64)).cuda(), torch.from_numpy(i % page).cuda()
+        cache.k[at[0], :, at[1]] *= ramp[:, None, None]
+    g = torch.Generator(device="cuda").manual_seed(11)
+    q = torch.randn(sum(counts), hq, 128, generator=g, device="cuda").to(torch.float32 if qt == "f32" else torch.bfloat16)
+    rng = np.random.default_rng(12)
+    rows = [S.tree_rows(random_parents(rng, c, "random")) for c in counts]
+    m = i32(np.concatenate([S.pack_rows(r, (n + 31) // 32) for r in rows]).view(np.int32))
+    qs = tsd.Queries(q, q_indptr=i32([0, n, n + 3]), max_tokens_per_seq=n)
+    out, lse = tsd.tree_decode(cache, qs, m, out_dtype=torch.float32)
+    check_tree(cache, table, page, q, counts, lens, rows, out, lse, qs.sm_scale or 1 / math.sqrt(128))
+
+
+@pytest.mark.parametrize("before", [6, 38, 59, 30, 2059])
+@pytest.mark.parametrize("qt", ["bf16", "f32"])
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_tree_nonfinite_drafts_anywhere_in_a_tile(what, qt, before):
+    """Two drafts whose V rows hold anything, in the first, the second and both halves of a tile, or in two tiles."""
+    import torch
+    n, hkv, G, page = 9, 2, 3, 4
+    cache, table = make_cache([before + n], hkv, page)
+    clean, _ = make_cache([before + n], hkv, page)
+    for d in (1, 5):
+        cache.v[table[0, (before + d) // page], :, (before + d) % page] = what
+    q = torch.randn(n, hkv * G, 128, device="cuda").to(torch.float32 if qt == "f32" else torch.bfloat16)
+    rows = S.tree_rows([-1, 0, 0, 2, 1, 2, 5, 3, -1])
+    m = i32(S.pack_rows(rows, 1).view(np.int32))
+    qs = tsd.Queries(q, q_indptr=i32([0, n]), max_tokens_per_seq=n)
+    for dt in (torch.float32, torch.bfloat16):
+        out, lse = tsd.tree_decode(cache, qs, m, out_dtype=dt)
+        ref, rl = tsd.tree_decode(clean, qs, m, out_dtype=dt)
+        sees = torch.tensor([bool(r & {1, 5}) for r in rows], device="cuda")
+        assert torch.equal(lse, rl)
+        assert torch.equal(out[~sees], ref[~sees]) and torch.isfinite(out[~sees]).all()
+        assert torch.isnan(out[sees]).all() if what != what else (out[sees] == what).all()
+
+
 def test_tree_bad_pages_and_sequences():
     import torch
     counts, before, page = [4, 4, 2], [300, 60, 33], 16
