@@ -151,7 +151,7 @@ constexpr int kTaThreads = 512;
 constexpr int kTaSoftmaxRegs = 192, kTaOtherRegs = 64;
 constexpr int kTaRowsPerStream = 128;
 constexpr int kTaTiles = 229376;               // Q tiles and the ring
-constexpr size_t kTaSmem = kTaTiles + 3072;    // then barriers and scratch: all of an SM's shared memory
+constexpr size_t kTaSmem = 227 * 1024;         // then barriers and scratch: all of an SM's shared memory
 
 template <int QP, int PP>
 struct TreeShape {
