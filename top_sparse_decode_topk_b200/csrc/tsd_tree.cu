@@ -377,8 +377,12 @@ __device__ __noinline__ uint64_t tree_visible(const TreeArgs& a, TreeSeq s, int 
   return v;
 }
 
-// The paths that few tiles take stand outside the softmax loop, so that they cost it no registers (168
-// a thread; what spills goes to L2, since shared memory takes nearly all of the L1).
+// The paths that few tiles take stand outside the softmax loop, so that they cost it no registers
+// (kTaSoftmaxRegs a thread; what spills goes to L2, since shared memory takes nearly all of the L1).
+// Tensor memory is read and written by whole warps: the instructions need all 32 lanes, converged.  Every
+// condition around one of these calls or such an instruction is therefore the same for a warp -- the role,
+// warp_live, the step's number, `special`, the tile's marks, a ballot -- and what a lane decides for itself
+// (valid, seen, m) is data: a factor, a mask or a store that is left out.
 
 // O of this warp's lists times f.
 __device__ __noinline__ void tree_scale(uint32_t to, float f) {
@@ -488,6 +492,7 @@ __device__ __noinline__ uint64_t tree_clean_v(unsigned char* vt, uint32_t* found
   }
   asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   if (threads == 256) named_sync(bar, threads);   // the other stream's products read these rows too
+  __syncwarp();   // tensor-memory instructions follow
   return any;
 }
 
@@ -737,9 +742,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           mbar_arrive(&ctl->s_free[s]);
         }
         if (warp_live) {
-          if (special || (bad0 | bad1)) {
+          if (special || (bad0 | bad1)) {   // the marks are the tile's: every lane comes here or none
             const uint64_t bad = (uint64_t)bad1 << 32 | bad0;
-            seen = valid ? tree_visible<TT>(a, sq, j, tile * TT) & ~bad : 0u;
+            seen = tree_visible<TT>(a, sq, valid ? j : 0, tile * TT) & ~bad;   // called by every lane
+            if (!valid) seen = 0;
+            __syncwarp();
 #pragma unroll
             for (int c = 0; c < TT; ++c) x[c] = seen >> c & 1 ? x[c] : -INFINITY;
           }
@@ -858,9 +865,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       // ---- the segment's state: O / l where the unit is whole, else a partial state
       float w0 = 1.f, w1 = 0.f;
       bool two = false;
-      if (SH::kFlush && m_sum != -INFINITY && warp_live) {   // the sums in global memory come on top
-        tree_unflush(to, sums, fast_exp2(m_sum - m), valid);
-      }
+      // The sums in global memory come on top.  Whether there are any is the same for a whole warp; a list that
+      // had seen nothing when they were moved last (m_sum -inf) has zeros there, which count for nothing.
+      if (SH::kFlush && steps > SH::kFlush && warp_live)
+        tree_unflush(to, sums, m_sum == -INFINITY ? 0.f : fast_exp2(m_sum - m), valid);
       if (!dual) {
         ctl->ml[s][row] = make_float2(m, l);
         tc_fence_before_sync();
