@@ -146,3 +146,15 @@ def test_a_bad_page_in_each_of_the_first_tiles(qt, kind):
 def test_nothing_but_bad_pages_before_the_drafts(qt):
     """All lists see their first token late."""
     run([70] * 30, [1600] * 30, 8, 2, qt, "f32", "custom", seed=5, check=(0, 11, 29), bad=list(range(0, 1600, 16)))
+
+
+@pytest.mark.parametrize("qt,ot", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32"), ("f32", "bf16")])
+def test_units_of_one_tile_between_longer_ones(qt, ot):
+    """Dozens of units of one tile in a CTA's share, with longer ones among and behind them."""
+    rng = np.random.default_rng(8)
+    lens = [int(rng.integers(1, 33)) for _ in range(700)]
+    for b in (5, 200, 201, 350, 699):
+        lens[b] = int(rng.integers(100, 900))
+    counts = [min(n, int(rng.integers(1, 4))) for n in lens]
+    run(counts, [n - c for n, c in zip(lens, counts)], 16, 8, qt, ot, "custom", seed=9,
+        check=list(range(0, 700, 29)) + [5, 200, 201, 202, 350, 699])

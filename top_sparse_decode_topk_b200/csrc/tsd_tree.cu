@@ -277,7 +277,10 @@ struct TreeCtl {
   // barriers' phase k / 2; s_full of step k implies that the products of step k - 2 are done, so no wait
   // is two phases behind.  Split: S has columns 0 to 63, free again (s_free) as soon as the softmax has
   // read it, P those behind it; p_ready[s][0] and o_done[s][0] count halves of steps.
-  uint64_t q_ready, s_full[2][2], s_free[2], p_ready[2][2], o_done[2][2], fixed[2], drain[2];
+  // q_ready[s] has a phase for each segment in which stream s has steps, since an issuer waits in those
+  // alone: in a segment of one tile nothing holds the others until stream 1's issuer has come by, which over
+  // a run of such segments could be more than one phase late.
+  uint64_t q_ready[2], s_full[2][2], s_free[2], p_ready[2][2], o_done[2][2], fixed[2], drain[2];
   uint32_t abort, tmem, nf[2][2];
   // Rows with a bad page of tile m (counted over the CTA's share), at m % 32: K is loaded at most
   // 4 (two steps of two streams) + kKSlots <= 12 tiles ahead of the softmax.
@@ -564,8 +567,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       mbar_init(&ctl->v_full[i], 1);
       mbar_init(&ctl->v_empty[i], 2);
     }
-    mbar_init(&ctl->q_ready, 256);
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl->q_ready[s], 256);
       for (int d = 0; d < 2; ++d) {
         mbar_init(&ctl->s_full[s][d], 1);
         mbar_init(&ctl->p_ready[s][d], 128);
@@ -701,7 +704,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
       }
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-      mbar_arrive(&ctl->q_ready);
+      mbar_arrive(&ctl->q_ready[0]);
+      if (dual || ntile > 1) mbar_arrive(&ctl->q_ready[1]);   // stream 1 has steps
 
       float m = -INFINITY, l = 0.f;
       float m_sum = -INFINITY;   // reference of the sums moved to global memory; -inf: none yet
@@ -1062,15 +1066,17 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       const uint64_t q_desc = sw128_desc(smem_u32(qtile), 1024), ring_k = sw128_desc(smem_u32(kring), 1024),
                      ring_v = sw128_mn_desc(smem_u32(vring), TT * 128, 1024);
       const uint32_t tm = tmem + s * 256;
-      uint32_t tiles_done = 0, done = 0, fixes = 0, segs = 0;
+      uint32_t tiles_done = 0, done = 0, fixes = 0, segs = 0;   // segs: those in which this stream has steps
 #pragma unroll 1
-      for (; wk.live(); wk.next(a, G), ++segs) {
+      for (; wk.live(); wk.next(a, G)) {
         const bool dual = wk.dual(G);
         const int ntile = wk.k1 - wk.k0, stride = dual ? 1 : 2, first = dual ? 0 : s;
         const int steps = (ntile - first + stride - 1) / stride;
         const uint64_t qd = q_desc + (dual && s ? 32768 >> 4 : 0);
-        tree_wait_warp(&ctl->q_ready, segs & 1, ctl, a.status);
-        tc_fence_after_sync();
+        if (steps > 0) {
+          tree_wait_warp(&ctl->q_ready[s], segs++ & 1, ctl, a.status);
+          tc_fence_after_sync();
+        }
         auto scores = [&](int i) {
           const uint32_t n = tiles_done + first + stride * i, slot = n % KS, buf = SH::kSplit ? 0 : (done + i) & 1;
           tree_wait_warp(&ctl->k_full[slot], (n / KS) & 1, ctl, a.status);
