@@ -66,16 +66,16 @@ class Meet:
 class Kernel:
     """segments: (tiles, both streams hold different lists, tiles at the end that are special)."""
 
-    def __init__(self, shape, segments, rng, one_q_ready=False):
+    def __init__(self, shape, segments, rng, one_q_ready=False, one_fixed=False):
         self.sh, self.segments, self.rng = shape, segments, rng
-        self.one_q = one_q_ready
+        self.one_q, self.one_fixed = one_q_ready, one_fixed
         b2 = lambda n: [[Bar(n), Bar(n)] for _ in range(2)]
         self.k_full, self.k_empty = [Bar(1) for _ in range(shape.ks)], [Bar(2) for _ in range(shape.ks)]
         self.v_full, self.v_empty = [Bar(1) for _ in range(shape.vs)], [Bar(2) for _ in range(shape.vs)]
         self.q_ready = [Bar(2), Bar(2)]
         self.s_full, self.p_ready, self.o_done = b2(1), b2(1), b2(1)
         self.s_free = [Bar(1), Bar(1)]
-        self.fixed = [Bar(1), Bar(1)]
+        self.fixed = b2(1)
         self.meet = Meet()
         self.k_tile, self.v_tile = [None] * shape.ks, [None] * shape.vs   # what a slot holds
         self.sp = [[None, None], [None, None]]     # what a stream's S and P buffers hold
@@ -147,7 +147,7 @@ class Kernel:
                 yield from self.together()
 
     def arrive_fixed(self, s, step):
-        self.fixed[s].arrive()
+        self.fixed[s][0 if self.one_fixed else step & 1].arrive()
 
     def products_done(self, s, step):
         if self.sh.split:
@@ -224,8 +224,9 @@ class Kernel:
             tiles_done, done = tiles_done + ntile, done + steps
 
     def wait_fixed(self, s, step, fixes):
-        fixes[0] += 1
-        yield lambda: self.fixed[s].done(fixes[0] - 1)
+        buf = 0 if self.one_fixed else step & 1
+        fixes[buf] += 1
+        yield lambda: self.fixed[s][buf].done(fixes[buf] - 1)
 
     def producer(self, is_v, odd):
         full, empty, tile = (self.v_full, self.v_empty, self.v_tile) if is_v else (self.k_full, self.k_empty, self.k_tile)
@@ -302,7 +303,7 @@ def test_waits_are_at_most_a_phase_away(qp, pp, starve):
     assert shape.ks % 2 == 0 and shape.vs % 2 == 0
     for seed in range(6):
         rng = random.Random(seed)
-        Kernel(shape, draw_segments(rng, shape, [0]), rng).run(starve)
+        Kernel(shape, draw_segments(rng, shape, [0, 1, 2, 3, 9]), rng).run(starve)
     # runs of units of one tile, with longer ones behind them
     for seed in range(3):
         rng = random.Random(seed)
@@ -314,3 +315,10 @@ def test_one_barrier_for_both_issuers_would_not_do():
     rng = random.Random(0)
     with pytest.raises(AssertionError, match="waits for phase"):
         Kernel(Shape(1, 1), [(1, False, 0)] * 5 + [(6, False, 0)], rng, one_q_ready=True).run(("issuer", 1))
+
+
+def test_one_barrier_for_both_buffers_would_not_do():
+    """The same for `fixed`: two special steps in a row with more behind them."""
+    rng = random.Random(0)
+    with pytest.raises(AssertionError, match="waits for phase"):
+        Kernel(Shape(1, 1), [(12, True, 9)] * 3, rng, one_fixed=True).run(("issuer", 0))

@@ -279,8 +279,10 @@ struct TreeCtl {
   // read it, P those behind it; p_ready[s][0] and o_done[s][0] count halves of steps.
   // q_ready[s] has a phase for each segment in which stream s has steps, since an issuer waits in those
   // alone: in a segment of one tile nothing holds the others until stream 1's issuer has come by, which over
-  // a run of such segments could be more than one phase late.
-  uint64_t q_ready[2], s_full[2][2], s_free[2], p_ready[2][2], o_done[2][2], fixed[2], drain[2];
+  // a run of such segments could be more than one phase late.  fixed[s][buf] (not split): a special step is through
+  // with the P of its buffer.  The scores of the step after it are made already, so its fixed can come before the
+  // issuer has waited for this one's: hence one for each buffer.
+  uint64_t q_ready[2], s_full[2][2], s_free[2], p_ready[2][2], o_done[2][2], fixed[2][2], drain[2];
   uint32_t abort, tmem, nf[2][2];
   // Rows with a bad page of tile m (counted over the CTA's share), at m % 32: K is loaded at most
   // 4 (two steps of two streams) + kKSlots <= 12 tiles ahead of the softmax.
@@ -573,9 +575,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         mbar_init(&ctl->s_full[s][d], 1);
         mbar_init(&ctl->p_ready[s][d], 128);
         mbar_init(&ctl->o_done[s][d], 1);
+        mbar_init(&ctl->fixed[s][d], 128);
       }
       mbar_init(&ctl->s_free[s], 128);
-      mbar_init(&ctl->fixed[s], 128);
       mbar_init(&ctl->drain[s], 1);
     }
     ctl->abort = 0;
@@ -830,7 +832,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
               tree_add_nonfinite<SH::PT, PP>(a.kv, wk.b, wk.g, tile * TT, odd, seen, tb, to);
               tc_fence_before_sync();
             }
-            if (i + 2 < steps) mbar_arrive(&ctl->fixed[s]);
+            if (i + 2 < steps) mbar_arrive(&ctl->fixed[s][buf]);
           }
         } else {
           if (special) clean_v();
@@ -1066,7 +1068,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       const uint64_t q_desc = sw128_desc(smem_u32(qtile), 1024), ring_k = sw128_desc(smem_u32(kring), 1024),
                      ring_v = sw128_mn_desc(smem_u32(vring), TT * 128, 1024);
       const uint32_t tm = tmem + s * 256;
-      uint32_t tiles_done = 0, done = 0, fixes = 0, segs = 0;   // segs: those in which this stream has steps
+      uint32_t tiles_done = 0, done = 0, segs = 0;   // segs: those in which this stream has steps
+      uint32_t fixes = 0;                            // bit b: parity of the next phase of fixed[s][b]
 #pragma unroll 1
       for (; wk.live(); wk.next(a, G)) {
         const bool dual = wk.dual(G);
@@ -1122,7 +1125,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             }
             if (i + 2 < steps) {
               if (i >= 0 && (wk.k0 + at + 1) * TT > wk.s.base) {   // a special tile: P is read once more
-                tree_wait_warp(&ctl->fixed[s], fixes++ & 1, ctl, a.status);
+                const uint32_t buf = (done + i) & 1;
+                tree_wait_warp(&ctl->fixed[s][buf], fixes >> buf & 1, ctl, a.status);
+                fixes ^= 1u << buf;
                 tc_fence_after_sync();
               }
               scores(i + 2);
