@@ -4,7 +4,9 @@ A wait on an mbarrier names a phase by its parity alone: it is right when the ph
 the one before.  The model runs the kernel's roles -- two softmax streams, two MMA issuers, four producers, and the
 copies and products that complete by themselves -- over barriers that count phases, in random orders and with one role
 starved at a time, and fails when a wait is further away from its barrier, when an arrival comes too many, when a
-buffer is used before or after its time, or when nobody can go on.
+buffer is used before or after its time, when nobody can go on, or when a copy or product is under way at the end.  Where
+a wait gives up, all waits but the last ones (for copies and products in flight) let everybody through, and what
+the buffers hold no longer matters.
 """
 
 import random
@@ -66,9 +68,11 @@ class Meet:
 class Kernel:
     """segments: (tiles, both streams hold different lists, tiles at the end that are special)."""
 
-    def __init__(self, shape, segments, rng, one_q_ready=False, one_fixed=False):
+    def __init__(self, shape, segments, rng, one_q_ready=False, one_fixed=False, give_up_at=None,
+                 copies_go_on=False):
         self.sh, self.segments, self.rng = shape, segments, rng
-        self.one_q, self.one_fixed = one_q_ready, one_fixed
+        self.one_q, self.one_fixed, self.copies_go_on = one_q_ready, one_fixed, copies_go_on
+        self.give_up_at, self.abort = give_up_at, False   # the number of moves after which a wait gives up
         b2 = lambda n: [[Bar(n), Bar(n)] for _ in range(2)]
         self.k_full, self.k_empty = [Bar(1) for _ in range(shape.ks)], [Bar(2) for _ in range(shape.ks)]
         self.v_full, self.v_empty = [Bar(1) for _ in range(shape.vs)], [Bar(2) for _ in range(shape.vs)]
@@ -105,7 +109,7 @@ class Kernel:
                     yield from self.products_done(s, step - 1)
                 phase = step if sh.split else step >> 1
                 yield lambda: self.s_full[s][buf].done(phase)
-                assert self.sp[s][buf] == ("S", step)
+                self.holds(self.sp[s][buf] == ("S", step))
                 if sh.split:
                     self.s_free[s].arrive()
                 if i > 0 and self.rng.random() < 0.3:       # a maximum grew
@@ -116,7 +120,7 @@ class Kernel:
                 odd = False
                 if special:
                     yield lambda: self.v_full[num % sh.vs].done(num // sh.vs)
-                    assert self.v_tile[num % sh.vs] == num
+                    self.holds(self.v_tile[num % sh.vs] == num)
                     if dual:
                         for _ in range(4):
                             yield from self.together()
@@ -126,7 +130,7 @@ class Kernel:
                     yield None
                     if special and odd:
                         yield from self.products_done(s, step)
-                        assert self.sp[s][buf] == ("P", step), "P is read once more"
+                        self.holds(self.sp[s][buf] == ("P", step))   # P is read once more
                     if special and i + 2 < steps:
                         self.arrive_fixed(s, step)
                 else:
@@ -139,7 +143,7 @@ class Kernel:
                         yield None
                         if special and odd:
                             yield lambda: self.o_done[s][0].done(2 * step + c)
-                            assert self.p[s] == (step, c)
+                            self.holds(self.p[s] == (step, c))
             if steps:
                 yield from self.products_done(s, done + steps - 1)
             done, tiles_done = done + steps, tiles_done + ntile
@@ -155,10 +159,13 @@ class Kernel:
         else:
             yield lambda: self.o_done[s][step & 1].done(step >> 1)
 
-    def together(self):
+    def together(self):   # bar.sync does not give up: both streams come to every one of them
         turn = self.meet.turns
         self.meet.come()
-        yield lambda: self.meet.turns > turn
+        yield "always", lambda: self.meet.turns > turn
+
+    def holds(self, right):
+        assert right or self.abort, "a buffer does not hold what its user expects"
 
     def issuer(self, s):
         sh, tiles_done, done, segs, fixes = self.sh, 0, 0, 0, [0, 0]
@@ -177,7 +184,7 @@ class Kernel:
                 yield lambda: self.k_full[slot].done(n // sh.ks)
 
                 def mma():
-                    assert self.k_tile[slot] == n and self.q[0 if not dual else s] == seg
+                    self.holds(self.k_tile[slot] == n and self.q[s if dual else 0] == seg)
                     self.sp[s][buf] = ("S", step)
                 self.pipe[s] += [mma, self.s_full[s][buf].arrive, self.k_empty[slot].arrive]
                 if not dual:
@@ -189,8 +196,8 @@ class Kernel:
                 slot = n % sh.vs
 
                 def mma():
-                    assert self.v_tile[slot] == n
-                    assert (self.p[s] == (step, c)) if sh.split else (self.sp[s][step & 1] == ("P", step))
+                    self.holds(self.v_tile[slot] == n)
+                    self.holds((self.p[s] == (step, c)) if sh.split else (self.sp[s][step & 1] == ("P", step)))
                 self.pipe[s] += [mma, self.o_done[s][0 if sh.split else step & 1].arrive]
                 if c != 0:
                     self.pipe[s] += [self.v_empty[slot].arrive] * (1 if dual else 2)
@@ -222,6 +229,7 @@ class Kernel:
                         yield lambda: self.p_ready[s][0].done(2 * step + c)
                         yield from products(i, c)
             tiles_done, done = tiles_done + ntile, done + steps
+        yield "always", lambda: not self.pipe[s]
 
     def wait_fixed(self, s, step, fixes):
         buf = 0 if self.one_fixed else step & 1
@@ -230,20 +238,24 @@ class Kernel:
 
     def producer(self, is_v, odd):
         full, empty, tile = (self.v_full, self.v_empty, self.v_tile) if is_v else (self.k_full, self.k_empty, self.k_tile)
-        slots, n = len(full), 0
-        for ntile, _, _ in self.segments:
-            for _ in range(ntile):
-                if n % 2 == odd:
-                    slot, at = n % slots, n // slots
-                    if at > 0:
-                        yield lambda: empty[slot].done(at - 1)
-                    full[slot].arrive(tx=1)
-                    self.copies.append((full[slot], tile, slot, n))
-                    yield None
-                n += 1
-        for i in range(max(0, n - slots), n):
-            # tiles of the other producer may be further away; that producer waits for them itself
-            yield lambda: (full[i % slots].phase - 1 - i // slots) % 2 == 0
+        slots, n, stop = len(full), 0, False
+        for n in range(sum(ntile for ntile, _, _ in self.segments)):
+            if n % 2 != odd:
+                continue
+            slot, at = n % slots, n // slots
+            if at > 0:
+                yield lambda: empty[slot].done(at - 1)
+                if self.abort and not self.copies_go_on:
+                    stop = True
+                    break
+            full[slot].arrive(tx=1)
+            self.copies.append((full[slot], tile, slot, n))
+            yield None
+        end = n if stop else n + 1
+        for i in range(max(0, end - slots), end):
+            if i % 2 == odd:
+                wait = lambda: full[i % slots].done(i // slots)
+                yield wait if self.copies_go_on else ("always", wait)
 
     # ---- what completes by itself
     def hardware(self, which):
@@ -269,18 +281,26 @@ class Kernel:
             if r[0] == "hardware":
                 return self.hardware(r[1])
             w = waits[r]
-            if w == "end" or (w is not None and not w()):
+            if w == "end":
+                return False
+            if isinstance(w, tuple):
+                if not w[1]():
+                    return False
+            elif w is not None and not self.abort and not w():
                 return False
             waits[r] = next(roles[r], "end")
             return True
 
-        while True:
+        moves = 0
+        while any(w != "end" for w in waits.values()):
+            moves += 1
+            self.abort = self.abort or moves == self.give_up_at
             order = [r for r in keys if r != starve]
             self.rng.shuffle(order)
             if not any(move(r) for r in order) and not (starve is not None and move(starve)):
                 break
         assert all(w == "end" for w in waits.values()), {r: "waits" for r, w in waits.items() if w != "end"}
-        assert not self.copies and not any(self.pipe)
+        assert not self.copies and not any(self.pipe), "under way at the end"
 
 
 SHAPES = [(1, 1), (3, 1), (1, 3), (3, 3)]
@@ -301,7 +321,7 @@ def draw_segments(rng, shape, special):
 def test_waits_are_at_most_a_phase_away(qp, pp, starve):
     shape = Shape(qp, pp)
     assert shape.ks % 2 == 0 and shape.vs % 2 == 0
-    for seed in range(6):
+    for seed in range(4):
         rng = random.Random(seed)
         Kernel(shape, draw_segments(rng, shape, [0, 1, 2, 3, 9]), rng).run(starve)
     # runs of units of one tile, with longer ones behind them
@@ -322,3 +342,25 @@ def test_one_barrier_for_both_buffers_would_not_do():
     rng = random.Random(0)
     with pytest.raises(AssertionError, match="waits for phase"):
         Kernel(Shape(1, 1), [(12, True, 9)] * 3, rng, one_fixed=True).run(("issuer", 0))
+
+
+@pytest.mark.parametrize("starve", STARVED)
+@pytest.mark.parametrize("qp,pp", SHAPES)
+def test_a_wait_that_gives_up_leaves_nothing_under_way(qp, pp, starve):
+    shape = Shape(qp, pp)
+    for seed in range(12):
+        rng = random.Random(seed)
+        Kernel(shape, draw_segments(rng, shape, [0, 1, 3]), rng, give_up_at=rng.randint(1, 150)).run(starve)
+
+
+def test_copies_behind_a_wait_that_gave_up_would_not_do():
+    """The model sees what producers that went on would do: arrivals too many, or copies in flight at the end."""
+    seen = set()
+    for seed in range(40):
+        rng = random.Random(seed)
+        segments = draw_segments(rng, Shape(1, 1), [0, 1, 3])
+        try:
+            Kernel(Shape(1, 1), segments, rng, give_up_at=rng.randint(1, 60), copies_go_on=True).run(("hardware", 2))
+        except AssertionError as e:
+            seen.add(str(e).split("\n")[0])
+    assert seen == {"an arrival too many", "under way at the end"}

@@ -1,6 +1,7 @@
 // Trees of drafted tokens: ancestor masks, and decode attention in which a draft sees the tokens
 // before the drafts and the drafts named by its mask.
 #include <math.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include "tsd_host.h"
@@ -127,7 +128,8 @@ __global__ void __launch_bounds__(kTmThreads) tree_mask_kernel(TreeMaskArgs a) {
 // products are then added for those lists alone that see them.
 //
 // Every wait is bounded; a wait that gives up raises `abort`, after which all waits return at once,
-// the loops run out, and the CTA ends with TSD_DEV_TIMEOUT set.
+// the producers issue no more copies, the other loops run out over whatever the buffers hold, and the CTA ends with
+// TSD_DEV_TIMEOUT set once its copies and MMAs in flight are through (waited for apart from `abort`).
 struct TreeArgs {
   KvView kv;
   QView qv;
@@ -143,6 +145,7 @@ struct TreeArgs {
   float4* part_acc;    // [2 * CTAs][32][part_rows] four dims of an unnormalised row
   float4* sums;        // [CTAs][2][32][128] sums of a stream's products (fp32 outputs)
   int32_t ctas;
+  uint32_t tries;      // of up to a microsecond each, after which a wait gives up
 };
 
 constexpr int kTaThreads = 512;
@@ -283,7 +286,7 @@ struct TreeCtl {
   // with the P of its buffer.  The scores of the step after it are made already, so its fixed can come before the
   // issuer has waited for this one's: hence one for each buffer.
   uint64_t q_ready[2], s_full[2][2], s_free[2], p_ready[2][2], o_done[2][2], fixed[2][2], drain[2];
-  uint32_t abort, tmem, nf[2][2];
+  uint32_t abort, tries, tmem, nf[2][2];
   // Rows with a bad page of tile m (counted over the CTA's share), at m % 32: K is loaded at most
   // 4 (two steps of two streams) + kKSlots <= 12 tiles ahead of the softmax.
   uint32_t bad[32][2];
@@ -292,14 +295,14 @@ struct TreeCtl {
 };
 static_assert(sizeof(TreeCtl) <= kTaSmem - kTaTiles, "control block");
 
-// Bounded wait that gives way to `abort`: up to 2^20 tries of up to a microsecond each.  Counted, not
+// Bounded wait that gives way to `abort`: up to c->tries tries of up to a microsecond each.  Counted, not
 // timed, to keep the code small: the kernel's waits are many, and an instruction cache miss costs
 // a warp some hundred cycles.
 __device__ __forceinline__ void tree_wait(uint64_t* bar, uint32_t parity, TreeCtl* c, uint32_t* status) {
 #pragma unroll 1
   for (uint32_t tries = 0; !mbar_try_wait_suspend(bar, parity, 1000u);) {
     if (*reinterpret_cast<volatile uint32_t*>(&c->abort)) return;
-    if (++tries == 1u << 20) {
+    if (++tries >= c->tries) {
       atomicOr(&c->abort, 1u);
       flag_optional(status, TSD_DEV_TIMEOUT);
       return;
@@ -323,6 +326,11 @@ __device__ __forceinline__ void tree_wait_warp(uint64_t* bar, uint32_t parity, T
     tree_wait(bar, parity, c, status);
     __syncwarp();
   }
+}
+
+// Whether a wait of this CTA has given up, the same answer for the whole warp.
+__device__ __forceinline__ bool tree_gave_up(TreeCtl* c) {
+  return __any_sync(0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t*>(&c->abort) != 0);
 }
 
 template <int N>
@@ -581,6 +589,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       mbar_init(&ctl->drain[s], 1);
     }
     ctl->abort = 0;
+    ctl->tries = a.tries;
     ctl->b0 = ctl->off = 0;
     mbar_fence_init();
   }
@@ -967,8 +976,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const int page_rows = a.kv.hkv << shift, no_row = (int)(a.kv.num_pages * page_rows);   // no_row: zeros arrive
     const uint32_t num_pages = (uint32_t)a.kv.num_pages;
     uint32_t n = 0;
+    bool stop = false;
 #pragma unroll 1
-    for (; wk.live(); wk.next(a, G)) {
+    for (; wk.live() && !stop; wk.next(a, G)) {
       const int len = wk.s.len;
       // rows that no other unit reads are the first to leave L2
       const uint64_t pol = wk.s.mtiles == 1 ? l2_evict_first() : l2_evict_normal();
@@ -1014,7 +1024,13 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         const int box0 = w * per_tile, boxes = min(per_tile, (len - tile * TT + per - 1) / per);
         if (++w == window) w = 0;
         if ((n & 1) != odd) continue;
-        if (round > 0) tree_wait_warp(&empty[slot], (round - 1) & 1, ctl, a.status);
+        if (round > 0) {
+          tree_wait_warp(&empty[slot], (round - 1) & 1, ctl, a.status);
+          if (tree_gave_up(ctl)) {   // the slot may still be in use, and its barrier in the phase of its last copies
+            stop = true;
+            break;
+          }
+        }
         if (!is_v) {
           uint32_t* marks = ctl->bad[n & 31];
           if (lane < 2) marks[lane] = 0;
@@ -1055,9 +1071,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
       }
     }
-    // no copy may be in flight when the CTA ends
+    // No copy may be in flight when the CTA ends: the last tiles that this warp asked for (those below n), whether
+    // or not a wait has given up.
+    bool landed = true;
 #pragma unroll 1
-    for (uint32_t i = n > slots ? n - slots : 0; i < n; ++i) tree_wait_warp(&full[i % slots], (i / slots) & 1, ctl, a.status);
+    for (uint32_t i = n > slots ? n - slots : 0; i < n; ++i)
+      if ((i & 1) == odd) landed &= mbar_wait(&full[i % slots], (i / slots) & 1);
+    if (!landed) flag_optional(a.status, TSD_DEV_TIMEOUT);
+    __syncwarp();
   }
   else if (warp == 8 || warp == 9) {
     // ---- MMA issuers: one thread for each stream.  A step's products are followed by the scores of the
@@ -1400,6 +1421,8 @@ tsd_status tsd_tree_decode(const tsd_kv_cache* cache, const tsd_queries* queries
   a.part_ml = reinterpret_cast<float2*>(w + l.ml);
   a.part_acc = reinterpret_cast<float4*>(w + l.acc);
   a.sums = reinterpret_cast<float4*>(w + l.sums);
+  const char* tries = getenv("TSD_TREE_WAIT_TRIES");   // for the tests of waits that run out
+  a.tries = tries != nullptr ? (uint32_t)strtoul(tries, nullptr, 10) : 1u << 20;
   KvMaps maps;
   st = make_kv_maps(cache, &maps, a.out_f32 && !a.qv.q_f32 ? TreeShape<1, 3>::TT : TreeShape<3, 3>::TT, true);
   static_assert(TreeShape<3, 3>::TT == TreeShape<1, 1>::TT && TreeShape<3, 3>::TT == TreeShape<3, 1>::TT, "boxes of a tile");
