@@ -158,3 +158,20 @@ def test_units_of_one_tile_between_longer_ones(qt, ot):
     counts = [min(n, int(rng.integers(1, 4))) for n in lens]
     run(counts, [n - c for n, c in zip(lens, counts)], 16, 8, qt, ot, "custom", seed=9,
         check=list(range(0, 700, 29)) + [5, 200, 201, 202, 350, 699])
+
+
+@pytest.mark.parametrize("qt,ot", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32"), ("f32", "bf16")])
+def test_a_share_with_not_a_number_alone(qt, ot):
+    """The unit is cut where its drafts begin, and in that share a list sees nothing but a key of NaNs: its maximum
+    there is -inf as if it saw nothing, its sum is not a number, and neither may get lost in the merge."""
+    import torch
+    dts = {"bf16": torch.bfloat16, "f32": torch.float32}
+    for before in (32, 64, 128, 192, 256, 320):   # a whole number of tiles; shares of two or three
+        cache, table = filled([before + 3], 1, 16, before)
+        p = int(table[0, before // 16])
+        cache.k[p, :, 1] = float("nan")           # draft 1
+        q = torch.randn(3, 2, 128, device="cuda").to(dts[qt])
+        mask = i32([[1], [2], [5]])               # draft 1 sees itself alone among the drafts; the others do not see it
+        out, lse = tsd.tree_decode(cache, tsd.Queries(q, i32([0, 3]), 3), mask, out_dtype=dts[ot])
+        assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
+        assert torch.isfinite(out[[0, 2]]).all() and torch.isfinite(lse[[0, 2]]).all()

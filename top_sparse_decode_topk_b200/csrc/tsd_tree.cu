@@ -1266,16 +1266,18 @@ __global__ void __launch_bounds__(kTgThreads) tree_merge_kernel(const __grid_con
 #pragma unroll 2
     for (int p = s0 + warp; p < s1; p += kTgWarps) {
       const float2 ml = __ldcg(a.part_ml + slot(p) * a.part_rows + row);
-      const float w = ml.x == -INFINITY ? 0.f : (ml.x == m ? 1.f : fast_exp2(ml.x - m));
+      // a share in which the list saw nothing (l = 0) counts for nothing; one whose scores were all -inf or NaN
+      // has the maximum -inf and a sum that is not a number, which stays
+      const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : (ml.x == m ? 1.f : fast_exp2(ml.x - m));
       weight[p - s0][lane] = w;
-      if (ml.x != -INFINITY) l += w * ml.y;
+      if (ml.x != -INFINITY || w != 0.f) l += w * ml.y;
     }
     __syncthreads();
     for (int q = s0 + p0; q < s1; q += 2 * kAhead) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const float w = q + 2 * i < s1 ? weight[q + 2 * i - s0][lane] : 0.f;
-        if (w != 0.f) {   // a share in which the list saw nothing holds no numbers
+        if (w != 0.f) {   // else the share adds nothing, whatever its state holds
 #pragma unroll
           for (int d = 0; d < ND; ++d) {
             o[d].x += w * x[i][d].x;
