@@ -1,0 +1,81 @@
+"""What the speculative calls keep and write besides their outputs: workspaces, status words, tables, lengths."""
+
+import numpy as np
+import pytest
+
+import top_sparse_decode_topk_b200 as tsd
+from tests.test_gpu_speculative import Serving, i32, make_cache, status
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def no_flags_left():
+    status()
+    yield
+    assert status() == 0
+
+
+def test_a_workspace_keeps_the_status_of_its_calls():
+    """Other calls, other shapes and growth do not lose a bit that nobody has read."""
+    import torch
+    s = Serving(3, 4, 40, 12)
+    ws = tsd.Workspace("cuda")
+    s.resize([20, 8, 0])
+    tsd.cache_resize(s.layers, s.refs, i32([20, 40, 0]), workspace=ws)      # no pages for sequence 1
+    q = torch.randn(3, 2, 128, device="cuda").bfloat16()
+    cache, _ = make_cache([300, 200, 9], 2, 16)
+    ref = tsd.tree_decode(cache, tsd.Queries(q))
+    got = tsd.tree_decode(cache, tsd.Queries(q), workspace=ws)               # more scratch than the call before
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    tsd.dense_decode(cache, tsd.Queries(q), workspace=ws)
+    tsd.decode_step(cache, tsd.Queries(q), 32, workspace=ws)
+    qs = tsd.Queries(torch.randn(60, 16, 128, device="cuda"), i32([0, 20, 40, 60]), 20)
+    tsd.tree_decode(cache, qs, out_dtype=torch.float32, workspace=ws)        # sequence 2 holds 9 tokens, not 20 drafts
+    assert tsd.read_device_status(ws) == tsd.DEV_NO_PAGES | tsd.DEV_BAD_SEQ
+    assert tsd.read_device_status(ws) == 0
+    s.check()
+
+
+def test_scratch_of_these_calls_leaves_the_other_calls_state_alone():
+    """A captured dense step whose workspace is zero at the start of every replay, though tree_decode uses it too."""
+    import torch
+    cache, _ = make_cache([3000, 200, 9000], 2, 16)
+    q = torch.randn(3, 4, 128, device="cuda").bfloat16()
+    qs = tsd.Queries(q)
+    ws = tsd.Workspace("cuda")
+    dense = [x.clone() for x in tsd.dense_decode(cache, qs)]
+    tree = [x.clone() for x in tsd.tree_decode(cache, qs, workspace=ws)]
+    tsd.dense_decode(cache, qs, workspace=ws)
+    torch.cuda.synchronize()
+    before = ws.buf.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a = tsd.dense_decode(cache, qs, workspace=ws)
+        b = tsd.tree_decode(cache, qs, workspace=ws)
+    for _ in range(3):
+        for x in (*a, *b):
+            x.fill_(9)
+        g.replay()
+        assert all(torch.equal(x, y) for x, y in zip(a, dense)) and all(torch.equal(x, y) for x, y in zip(b, tree))
+        tsd.tree_decode(cache, tsd.Queries(torch.randn(3, 32, 128, device="cuda")), out_dtype=torch.float32, workspace=ws)
+    tsd.tree_decode(cache, qs, workspace=ws)
+    assert ws.buf.numel() == before.numel() and torch.equal(ws.buf[:256], before[:256])
+    del g
+    assert tsd.read_device_status(ws) == 0
+
+
+def test_a_status_word_is_not_made_during_a_capture(monkeypatch):
+    import torch
+    cache, _ = make_cache([30, 20], 2, 16)
+    qs = tsd.Queries(torch.randn(2, 4, 128, device="cuda"))
+    want = tsd.tree_decode(cache, qs)
+    ws, parents = tsd.Workspace("cuda"), i32([-1])   # made here: no copies from the host in a capture
+    with pytest.raises(RuntimeError, match="before capturing"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            tsd.tree_decode(cache, qs, workspace=ws)
+    monkeypatch.setattr(tsd.speculative, "_STATUS", {})
+    with pytest.raises(RuntimeError, match="before capturing"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            tsd.tree_mask(parents)
+    assert all(torch.equal(a, b) for a, b in zip(tsd.tree_decode(cache, qs, workspace=ws), want))

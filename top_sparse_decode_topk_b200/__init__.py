@@ -321,12 +321,15 @@ class Queries:
 class Workspace:
     """Device scratch for the library calls (zero-initialised; the library keeps its
     leading region zero between calls).  Grows on demand; re-zeroed when the
-    cache/query shapes change."""
+    cache/query shapes change.  The calls of ``speculative`` have a buffer and a status word of
+    their own in it: they need no zeros, and neither clear the other calls' state nor lose theirs."""
 
     def __init__(self, device=None):
         self.device = device
         self.buf = None
         self.key = None
+        self.spec_status = None
+        self.spec_bufs = []   # the last one is in use
 
     def get(self, nbytes: int, key, stream) -> "object":
         import torch
@@ -337,6 +340,18 @@ class Workspace:
             _check(load_library().tsd_workspace_init(self.buf.data_ptr(), self.buf.numel(), stream), "workspace_init")
             self.key = key
         return self.buf
+
+    def spec_scratch(self, nbytes: int, device) -> "object":
+        """Scratch of the speculative calls, not initialised.  It grows by doubling, and outgrown buffers are kept
+        (less than the last one's size in all): a captured graph or another stream may still use them."""
+        import torch
+        old = self.spec_bufs[-1] if self.spec_bufs else None
+        if old is not None and old.device != device:
+            raise ValueError(f"the workspace holds memory of {old.device}, the cache is on {device}")
+        if old is None or old.numel() < nbytes:
+            self.spec_bufs.append(torch.empty(max(nbytes, 256, 0 if old is None else 2 * old.numel()),
+                                              dtype=torch.uint8, device=device))
+        return self.spec_bufs[-1]
 
 
 _DEFAULT_WS = {}
@@ -737,6 +752,8 @@ def read_device_status(workspace: Optional[Workspace] = None, device=None, strea
     flags = 0
     if ws.buf is not None:
         flags |= _read_status(ws.buf.data_ptr(), ws.buf.device, stream)
+    if ws.spec_status is not None:
+        flags |= _read_status(ws.spec_status.data_ptr(), ws.spec_status.device, stream)
     if workspace is None:
         word = speculative._STATUS.get(dev.index if dev.index is not None else torch.cuda.current_device())
         if word is not None:

@@ -10,8 +10,9 @@
     cache_resize(caches, refs, new_lens)               # the rejected drafts' pages go back
     cache_fork(caches, refs, src, dst)                 # sequences that share src's pages
 
-A step without new tokens (T = 0) is allowed and does nothing.  All tensors are on the cache's device.  Nothing here waits for the device, so every call can be
-captured into a CUDA graph (call it once before, so that the status word below exists).
+A step without new tokens (T = 0) is allowed and does nothing.  All tensors are on the cache's device.  Nothing here
+waits for the device, so every call can be captured into a CUDA graph.  The first call on a device, and the first
+with a new workspace, makes the status word below, and is refused during a capture: make it before.
 
 Outputs and scratch are allocated per call on the call's stream unless the caller passes them, so
 calls on several streams and several captured graphs share nothing.  Device-detected problems set
@@ -79,6 +80,15 @@ def _raw_stream(dev):
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
+def _status_word(device):
+    """A status word, cleared before any stream may use it."""
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("the status word of this device or workspace does not exist yet: make a call before capturing")
+    word = torch.zeros(64, dtype=torch.int32, device=device)
+    torch.cuda.current_stream(device).synchronize()   # once: other streams may use it at once
+    return word
+
+
 def _status_ptr(status, device):
     if status is not None:
         if status.dtype != torch.int32 or status.device != device or status.numel() < 1:
@@ -86,9 +96,7 @@ def _status_ptr(status, device):
         return status.data_ptr()
     word = _STATUS.get(device.index)
     if word is None:
-        word = _STATUS[device.index] = torch.zeros(64, dtype=torch.int32, device=device)
-        if not torch.cuda.is_current_stream_capturing():
-            torch.cuda.current_stream(device).synchronize()   # once: other streams may use it at once
+        word = _STATUS.setdefault(device.index, _status_word(device))   # the first of several host threads' words
     return word.data_ptr()
 
 
@@ -274,7 +282,7 @@ def tree_decode(cache: KVCache, queries: Queries, mask=None, out=None, out_dtype
     if T == 0:
         return out, lse
     nbytes = _LIB.tsd_tree_decode_workspace_size(cs, qs, code)
-    ws, keep, sp = _scratch(workspace, nbytes, "tree_decode", dev, status)
+    ws, keep, sp = _scratch(workspace, nbytes, dev, status)
     st = _LIB.tsd_tree_decode(cs, qs, mp, out.data_ptr(), code, None if lse is None else lse.data_ptr(), ws, nbytes, sp,
                               _raw_stream(dev))
     if st:
@@ -282,15 +290,17 @@ def tree_decode(cache: KVCache, queries: Queries, mask=None, out=None, out_dtype
     return out, lse
 
 
-def _scratch(workspace, nbytes, what, dev, status):
-    """Scratch of `nbytes`: its pointer, its owner, and the status word to use.  A Workspace keeps its status
-    word in its first 256 bytes; the scratch lies behind them.  The key is one no other call uses: a call that
-    needs the workspace's first part zeroed finds another key and zeroes it."""
+def _scratch(workspace, nbytes, dev, status):
+    """Scratch of `nbytes`: its pointer, its owner, and the status word to use."""
     if workspace is None:
         buf = torch.empty(nbytes if nbytes > 256 else 256, dtype=torch.uint8, device=dev)
         return buf.data_ptr(), buf, _status_ptr(status, dev)
-    buf = workspace.get(nbytes + 256, what, _raw_stream(dev))
-    return buf.data_ptr() + 256, buf, buf.data_ptr() if status is None else _status_ptr(status, dev)
+    if workspace.spec_status is None:
+        word = _status_word(dev)
+        if workspace.spec_status is None:
+            workspace.spec_status = word
+    buf = workspace.spec_scratch(nbytes, dev)
+    return buf.data_ptr(), buf, _status_ptr(workspace.spec_status if status is None else status, dev)
 
 
 class LayerCaches:
@@ -357,7 +367,7 @@ def cache_resize(caches, refs, new_lens, workspace: Optional[Workspace] = None, 
     cs = _cache_struct(cache)
     lens = _int32(new_lens, "new_lens", dev, (cs.batch,))
     nbytes = _LIB.tsd_cache_resize_workspace_size(cs)
-    ws, keep, sp = _scratch(workspace, nbytes, "cache_resize", dev, status)
+    ws, keep, sp = _scratch(workspace, nbytes, dev, status)
     st = _LIB.tsd_cache_resize(cs, len(caches.caches), caches.c_layers, rp, lens, ws, nbytes, sp, _raw_stream(dev))
     if st:
         raise TsdError(st, "tsd_cache_resize")
