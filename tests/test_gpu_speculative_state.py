@@ -79,3 +79,30 @@ def test_a_status_word_is_not_made_during_a_capture(monkeypatch):
         with torch.cuda.graph(torch.cuda.CUDAGraph()):
             tsd.tree_mask(parents)
     assert all(torch.equal(a, b) for a, b in zip(tsd.tree_decode(cache, qs, workspace=ws), want))
+
+
+def test_a_table_or_lengths_that_cannot_be_updated_in_place_are_refused():
+    import torch
+    page = lambda: torch.zeros(12, 2, 4, 128, dtype=torch.bfloat16, device="cuda")
+    wide, state, refs = i32(np.full((3, 20), -1)), i32(np.zeros((3, 2))), i32(np.zeros(12))
+    lens = i32([0, 0, 0])
+    sliced = tsd.KVCache(page(), page(), lens, 40, page_table=wide[:, :10])
+    strided = tsd.KVCache(page(), page(), state[:, 0], 40, page_table=wide[:, :10].contiguous())
+    short = tsd.KVCache(page(), page(), lens, 40, page_table=i32(np.full((2, 10), -1)))
+    for cache in (sliced, strided, short):
+        with pytest.raises(ValueError):
+            tsd.cache_resize(cache, refs, i32([4, 0, 0]))
+        with pytest.raises(ValueError):
+            tsd.cache_fork(cache, refs, i32([0]), i32([1]))
+    x = torch.zeros(3, 4, 128, device="cuda")
+    for cache in (strided, short):      # reads that would go astray
+        with pytest.raises(ValueError):
+            tsd.tree_decode(cache, tsd.Queries(x))
+        with pytest.raises(ValueError):
+            tsd.rope_append(cache, tsd.RotaryEmbedding(), x, x[:, :2], x[:, :2])
+        with pytest.raises(ValueError):
+            tsd.cache_compact(cache, i32([[0]] * 3))
+    assert (wide == -1).all() and not state.any() and not refs.any() and not lens.any()
+    ok = tsd.KVCache(page(), page(), lens, 80, page_table=wide)
+    tsd.cache_resize(ok, refs, i32([4, 0, 0]))
+    assert wide[0, 0] == 0 and lens.tolist() == [4, 0, 0]

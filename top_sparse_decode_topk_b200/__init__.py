@@ -220,6 +220,8 @@ class KVCache:
     paged:      k, v [num_pages, num_kv_heads, page_size, 128]; page_table int32 [B, max_pages];
     contiguous: k, v [B, num_kv_heads, max_seq_len, 128]; page_table None.
     seq_lens: int32 [B] on the device; max_seq_len: host bound on every entry.
+    A page_table that is not contiguous is copied: later changes of the original do not reach the
+    cache, and cache_fork and cache_resize, which update the table in place, refuse it.
     """
     k: "object"
     v: "object"
@@ -242,7 +244,9 @@ class KVCache:
         if self.page_table is not None:
             if self.page_table.dtype != torch.int32 or self.page_table.dim() != 2:
                 raise ValueError("page_table must be an int32 [batch, max_pages] tensor")
-            self.page_table = self.page_table.contiguous()
+            if not self.page_table.is_contiguous():
+                self.page_table = self.page_table.contiguous()
+                self.__dict__["_table_copy"] = self.page_table   # calls that write the table refuse a copy
 
     @property
     def device(self):

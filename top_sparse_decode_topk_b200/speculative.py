@@ -107,6 +107,25 @@ def _int32(t, name, device, shape):
     return t.data_ptr()
 
 
+def _check_tables(cache):
+    """The kernels index seq_lens and page_table as dense arrays with a row for every sequence, and some write them."""
+    lens, table = cache.seq_lens, cache.page_table
+    if lens.dim() != 1 or not lens.is_contiguous():
+        raise ValueError("seq_lens must be a contiguous int32 [batch] tensor")
+    if table is None:
+        if cache.k.shape[0] < lens.shape[0]:
+            raise ValueError("contiguous cache: k and v must have a row for every entry of seq_lens")
+    elif table.device != cache.k.device or not table.is_contiguous() or table.shape[0] < lens.shape[0]:
+        raise ValueError("page_table must be a contiguous tensor on the cache's device with a row for every entry of seq_lens")
+
+
+def _check_written(cache):
+    """For the calls that update page_table in place."""
+    if cache.page_table is not None and cache.page_table is cache.__dict__.get("_table_copy"):
+        raise ValueError("the page_table given was not contiguous, so the cache holds a copy, and an update would not "
+                         "reach the original: give a contiguous table")
+
+
 def _cache_struct(cache):
     """cache.c_struct(), reused while the cache holds the same tensors at the same addresses."""
     kept = cache.__dict__.get("_spec_struct")
@@ -118,6 +137,7 @@ def _cache_struct(cache):
             return c
     if cache.k.device.type != "cuda":
         raise ValueError("the cache must be on a CUDA device")
+    _check_tables(cache)
     c = cache.c_struct()
     cache.__dict__["_spec_struct"] = (cache.k, cache.v, cache.seq_lens, cache.page_table, cache.max_seq_len, c)
     return c
@@ -312,6 +332,10 @@ class LayerCaches:
         if not caches:
             raise ValueError("at least one cache")
         c0 = caches[0]
+        _check_tables(c0)
+        if len(caches) > 1:
+            for c in caches:
+                _check_written(c)   # each would have its own copy
         for c in caches[1:]:
             if c.k.shape != c0.k.shape or c.device != c0.device or c.seq_lens.data_ptr() != c0.seq_lens.data_ptr() or \
                     int(c.max_seq_len) != int(c0.max_seq_len) or (c.page_table is None) != (c0.page_table is None) or \
@@ -342,6 +366,7 @@ def cache_fork(caches, refs, src, dst, status=None, stream=None) -> None:
     if _elsewhere(dev, stream):
         with _Guard(dev, stream):
             return cache_fork(caches, refs, src, dst, status)
+    _check_written(cache)
     n = src.shape[0]
     st = _LIB.tsd_cache_fork(_cache_struct(cache), _refs(refs, cache, dev), n, _int32(src, "src", dev, (n,)),
                              _int32(dst, "dst", dev, (n,)), _status_ptr(status, dev), _raw_stream(dev))
@@ -363,6 +388,7 @@ def cache_resize(caches, refs, new_lens, workspace: Optional[Workspace] = None, 
     if _elsewhere(dev, stream):
         with _Guard(dev, stream):
             return cache_resize(caches, refs, new_lens, workspace, status)
+    _check_written(cache)
     rp = _refs(refs, cache, dev)
     cs = _cache_struct(cache)
     lens = _int32(new_lens, "new_lens", dev, (cs.batch,))
