@@ -106,3 +106,23 @@ def test_a_table_or_lengths_that_cannot_be_updated_in_place_are_refused():
     ok = tsd.KVCache(page(), page(), lens, 80, page_table=wide)
     tsd.cache_resize(ok, refs, i32([4, 0, 0]))
     assert wide[0, 0] == 0 and lens.tolist() == [4, 0, 0]
+
+
+def test_pages_are_copied_in_the_tensors_that_the_caches_hold_now():
+    import torch
+    s = Serving(3, 8, 64, 20)
+    s.resize([21, 0, 0])
+    s.fork([0], [1])
+    old = s.kv.clone()
+    s.kv = s.kv + 1                      # a pool somewhere else
+    for i, c in enumerate(s.layers.caches):
+        c.k, c.v = s.kv[2 * i], s.kv[2 * i + 1]
+    s.model.data = s.data()
+    s.resize([21, 23, 0])                # the shared page is copied, in the new pool
+    before = s.kv.clone()
+    keep = i32([[-1, -1], [1, -1], [-1, -1]])
+    out = tsd.cache_compact(s.layers, keep, i32([0, 0, 2, 2]), 2, refs=s.refs)
+    assert out.tolist() == [21, 22, 0]
+    p = int(s.table[1, 2])
+    before[:, p, :, 5] = before[:, p, :, 6]
+    assert torch.equal(s.kv, before) and old.shape == before.shape

@@ -53,3 +53,28 @@ def test_a_copied_table_is_not_written():
     speculative._check_written(c)
     speculative._check_written(kv(lens, wide))
     tsd.LayerCaches([kv(lens, wide), kv(lens, wide)])
+
+
+def test_layers_follow_replaced_tensors():
+    lens, table = i32(3), i32(3, 4)
+    caches = [kv(lens, table) for _ in range(3)]
+    layers = tsd.LayerCaches(caches)
+    at = lambda: [(x.k, x.v) for x in layers.c_layers]
+    where = lambda: [(c.k.data_ptr(), c.v.data_ptr()) for c in caches]
+    assert at() == where()
+    caches[1].v = torch.zeros_like(caches[1].v)
+    assert at() == where()
+    for c in caches:                                   # a pool that has grown
+        c.k, c.v = (torch.zeros(9, 1, 4, 128, dtype=torch.bfloat16) for _ in range(2))
+    assert at() == where()
+    caches[2].k = torch.zeros(7, 1, 4, 128, dtype=torch.bfloat16)
+    caches[2].v = torch.zeros_like(caches[2].k)        # one layer smaller than the others
+    with pytest.raises(ValueError, match="share"):
+        layers.c_layers
+    caches[2].k = torch.zeros(9, 1, 4, 128, dtype=torch.bfloat16)
+    caches[2].v = torch.zeros(9, 1, 4, 256, dtype=torch.bfloat16)[..., ::2]
+    with pytest.raises(ValueError, match="contiguous"):
+        layers.c_layers
+    caches[2].v = torch.zeros(9, 1, 4, 128)
+    with pytest.raises(ValueError, match="bfloat16"):
+        layers.c_layers

@@ -107,9 +107,13 @@ def _int32(t, name, device, shape):
     return t.data_ptr()
 
 
-def _check_tables(cache):
-    """The kernels index seq_lens and page_table as dense arrays with a row for every sequence, and some write them."""
-    lens, table = cache.seq_lens, cache.page_table
+def _check_arrays(cache):
+    """The kernels index k, v, seq_lens and page_table as dense arrays with a row for every sequence, and some write
+    them.  A cache's fields may have been assigned since it was made, so k and v are looked at again too."""
+    k, v, lens, table = cache.k, cache.v, cache.seq_lens, cache.page_table
+    if k.dim() != 4 or k.shape != v.shape or k.shape[3] != 128 or k.dtype != v.dtype or str(k.dtype) != "torch.bfloat16" or \
+            not k.is_contiguous() or not v.is_contiguous() or v.device != k.device or lens.device != k.device:
+        raise ValueError("k and v must be contiguous bfloat16 tensors of one 4-d shape with head_dim 128, on one device")
     if lens.dim() != 1 or not lens.is_contiguous():
         raise ValueError("seq_lens must be a contiguous int32 [batch] tensor")
     if table is None:
@@ -137,7 +141,7 @@ def _cache_struct(cache):
             return c
     if cache.k.device.type != "cuda":
         raise ValueError("the cache must be on a CUDA device")
-    _check_tables(cache)
+    _check_arrays(cache)
     c = cache.c_struct()
     cache.__dict__["_spec_struct"] = (cache.k, cache.v, cache.seq_lens, cache.page_table, cache.max_seq_len, c)
     return c
@@ -325,24 +329,37 @@ def _scratch(workspace, nbytes, dev, status):
 
 class LayerCaches:
     """The layers of a model: KVCaches of one shape that share a page table and seq_lens, as the calls
-    below take them.  Made once and kept; the calls also take a KVCache or a list of them."""
+    below take them.  Made once and kept; the calls also take a KVCache or a list of them.  A cache whose k or v
+    is replaced afterwards is looked at anew by the next call."""
 
     def __init__(self, caches):
         caches = [caches] if isinstance(caches, KVCache) else list(caches)
         if not caches:
             raise ValueError("at least one cache")
-        c0 = caches[0]
-        _check_tables(c0)
+        self.caches = tuple(caches)
+        self._bind()
+
+    def _bind(self):
+        caches, c0 = self.caches, self.caches[0]
         if len(caches) > 1:
             for c in caches:
                 _check_written(c)   # each would have its own copy
-        for c in caches[1:]:
+        for c in caches:
+            _check_arrays(c)
             if c.k.shape != c0.k.shape or c.device != c0.device or c.seq_lens.data_ptr() != c0.seq_lens.data_ptr() or \
                     int(c.max_seq_len) != int(c0.max_seq_len) or (c.page_table is None) != (c0.page_table is None) or \
                     (c.page_table is not None and c.page_table.data_ptr() != c0.page_table.data_ptr()):
                 raise ValueError("the layers must share their page table, seq_lens and shapes")
-        self.caches = caches
-        self.c_layers = (_LayerC * len(caches))(*[_LayerC(c.k.data_ptr(), c.v.data_ptr()) for c in caches])
+        self._held = [(c, c.k, c.v) for c in caches]   # whose addresses these are
+        self._c_layers = (_LayerC * len(caches))(*[_LayerC(c.k.data_ptr(), c.v.data_ptr()) for c in caches])
+
+    @property
+    def c_layers(self):
+        for c, k, v in self._held:
+            if c.k is not k or c.v is not v:
+                self._bind()
+                break
+        return self._c_layers
 
     @staticmethod
     def of(caches) -> "LayerCaches":
@@ -394,7 +411,8 @@ def cache_resize(caches, refs, new_lens, workspace: Optional[Workspace] = None, 
     lens = _int32(new_lens, "new_lens", dev, (cs.batch,))
     nbytes = _LIB.tsd_cache_resize_workspace_size(cs)
     ws, keep, sp = _scratch(workspace, nbytes, dev, status)
-    st = _LIB.tsd_cache_resize(cs, len(caches.caches), caches.c_layers, rp, lens, ws, nbytes, sp, _raw_stream(dev))
+    layers = caches.c_layers
+    st = _LIB.tsd_cache_resize(cs, len(layers), layers, rp, lens, ws, nbytes, sp, _raw_stream(dev))
     if st:
         raise TsdError(st, "tsd_cache_resize")
 
@@ -428,7 +446,8 @@ def cache_compact(caches, keep, q_indptr=None, max_tokens_per_seq: int = 1, refs
         n, ip = 1, None
     else:
         n, ip = int(max_tokens_per_seq), _int32(q_indptr, "q_indptr", dev, (B + 1,))
-    st = _LIB.tsd_cache_compact(cs, len(caches.caches), caches.c_layers, ip, n * B, n, kp, k_max,
+    layers = caches.c_layers
+    st = _LIB.tsd_cache_compact(cs, len(layers), layers, ip, n * B, n, kp, k_max,
                                 None if refs is None else _refs(refs, cache, dev),
                                 _int32(out_lens, "out_lens", dev, (B,)), _status_ptr(status, dev), _raw_stream(dev))
     if st:
