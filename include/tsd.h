@@ -593,8 +593,8 @@ size_t tsd_cache_resize_workspace_size(const tsd_kv_cache* cache);
  * layers: host array of num_layers (1 .. 128) layers' K and V, each laid out like cache->k; pages
  *   are copied in all of them (cache->k and v only if they are among them).
  * ws: at least tsd_cache_resize_workspace_size bytes, 256-byte aligned, not initialised.
- * Errors: INVALID_ARGUMENT, UNSUPPORTED (contiguous layout, more than 128 layers),
- * WORKSPACE_TOO_SMALL, CUDA.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (contiguous layout, more than 128 layers or 65535 sequences,
+ * batch x (max_pages_per_seq + 1) of 2^31 or more), WORKSPACE_TOO_SMALL, CUDA.
  */
 tsd_status tsd_cache_resize(const tsd_kv_cache* cache, int32_t num_layers, const tsd_layer* layers, int32_t* refs,
                             const int32_t* new_lens, void* ws, size_t ws_bytes, uint32_t* status,

@@ -1,10 +1,13 @@
 """Tables, lengths and layers that the speculative calls refuse, without a GPU."""
 
+import ctypes
+
 import pytest
 import torch
 
 import top_sparse_decode_topk_b200 as tsd
-from top_sparse_decode_topk_b200 import speculative
+from tests.test_abi import FAKE, fake_pointer_call, lib, make_cache   # noqa: F401
+from top_sparse_decode_topk_b200 import _LayerC, speculative
 
 
 def kv(lens, table, pages=5, max_len=16):
@@ -78,3 +81,18 @@ def test_layers_follow_replaced_tensors():
     caches[2].v = torch.zeros(9, 1, 4, 128)
     with pytest.raises(ValueError, match="bfloat16"):
         layers.c_layers
+
+
+@fake_pointer_call
+def test_pages_wanted_fit_32_bits(lib):
+    """The pages that all sequences may want together are summed in 32 bits: more are refused on the host."""
+    def resize(**kw):
+        c = make_cache(page_size=1, max_seq_len=100, **kw)
+        ls = (_LayerC * 1)(_LayerC(FAKE, FAKE))
+        return lib.tsd_cache_resize(ctypes.byref(c), 1, ls, FAKE, FAKE, FAKE, 64, None, None)   # 64 bytes are never enough
+    small = tsd.TSD_ERR_WORKSPACE_TOO_SMALL
+    assert resize(batch=60000, max_pages=35790) == small                      # 60000 x 35791 = 2^31 - 23648
+    assert resize(batch=60000, max_pages=35791) == tsd.TSD_ERR_UNSUPPORTED
+    assert resize(batch=1, max_pages=2 ** 31 - 2) == small
+    assert resize(batch=1, max_pages=2 ** 31 - 1) == tsd.TSD_ERR_UNSUPPORTED
+    assert resize(batch=2, max_pages=2 ** 30) == tsd.TSD_ERR_UNSUPPORTED

@@ -517,6 +517,8 @@ tsd_status tsd_cache_resize(const tsd_kv_cache* cache, int32_t num_layers, const
   if (st != TSD_OK) return st;
   if (new_lens == nullptr || ws == nullptr || ((uintptr_t)ws & 255) != 0) return TSD_ERR_INVALID_ARGUMENT;
   if (a.p.num_pages > 0x7fffffffLL || a.p.batch > 65535) return TSD_ERR_UNSUPPORTED;
+  // the pages that all sequences want, a copy each among them, are summed in 32 bits
+  if ((int64_t)a.p.batch * ((int64_t)a.p.max_pages + 1) > 0x7fffffffLL) return TSD_ERR_UNSUPPORTED;
   const ResizeLayout l = resize_layout(a.p.batch, a.p.num_pages);
   if (ws_bytes < l.total) return TSD_ERR_WORKSPACE_TOO_SMALL;
   char* w = static_cast<char*>(ws);
