@@ -126,3 +126,21 @@ def test_pages_are_copied_in_the_tensors_that_the_caches_hold_now():
     p = int(s.table[1, 2])
     before[:, p, :, 5] = before[:, p, :, 6]
     assert torch.equal(s.kv, before) and old.shape == before.shape
+
+
+@pytest.mark.parametrize("ip", [[2, 6, 9], [0, 4, 7], [1000, 1004, 1007], [2 ** 31 - 8, 2 ** 31 - 4, 2 ** 31 - 1]])
+def test_compact_takes_any_range_of_tokens(ip):
+    """Ranges that do not start at 0, as rope_append and tree_decode take them."""
+    import torch
+    cache, table = make_cache([14, 23], 2, 4, fill="other")
+    k, v = cache.k.clone(), cache.v.clone()
+    out = tsd.cache_compact(cache, i32([[1, 3], [0, 2]]), i32(ip), 4)
+    assert out.tolist() == [12, 22]
+    for b, dst, src in ((0, 10, 11), (0, 11, 13), (1, 21, 22)):
+        d, s = (int(table[b, dst // 4]), dst % 4), (int(table[b, src // 4]), src % 4)
+        for x in (k, v):
+            x[d[0], :, d[1]] = x[s[0], :, s[1]].clone()
+    assert torch.equal(cache.k, k) and torch.equal(cache.v, v)
+    tsd.cache_compact(cache, i32([[1, 3], [0, 2]]), i32([2, 7, 9]), 4)   # five drafts are above the bound, and draft 2 of two
+    assert status() == tsd.DEV_BAD_SEQ | tsd.DEV_BAD_INDEX
+    assert torch.equal(cache.k, k) and torch.equal(cache.v, v)

@@ -443,11 +443,11 @@ def cache_compact(caches, keep, q_indptr=None, max_tokens_per_seq: int = 1, refs
         raise TsdError(TSD_ERR_INVALID_ARGUMENT, "keep must have room for one draft")
     kp = _int32(keep, "keep", dev, (B, k_max))
     if q_indptr is None:
-        n, ip = 1, None
-    else:
-        n, ip = int(max_tokens_per_seq), _int32(q_indptr, "q_indptr", dev, (B + 1,))
+        n, ip, T = 1, None, B
+    else:   # only its gaps count: nothing here is indexed by token, so there is no number of tokens to keep within
+        n, ip, T = int(max_tokens_per_seq), _int32(q_indptr, "q_indptr", dev, (B + 1,)), 0x7FFFFFFF
     layers = caches.c_layers
-    st = _LIB.tsd_cache_compact(cs, len(layers), layers, ip, n * B, n, kp, k_max,
+    st = _LIB.tsd_cache_compact(cs, len(layers), layers, ip, T, n, kp, k_max,
                                 None if refs is None else _refs(refs, cache, dev),
                                 _int32(out_lens, "out_lens", dev, (B,)), _status_ptr(status, dev), _raw_stream(dev))
     if st:
