@@ -144,3 +144,38 @@ def test_compact_takes_any_range_of_tokens(ip):
     tsd.cache_compact(cache, i32([[1, 3], [0, 2]]), i32([2, 7, 9]), 4)   # five drafts are above the bound, and draft 2 of two
     assert status() == tsd.DEV_BAD_SEQ | tsd.DEV_BAD_INDEX
     assert torch.equal(cache.k, k) and torch.equal(cache.v, v)
+
+
+def test_trees_of_different_sizes_from_several_host_threads():
+    """Each thread's calls find the shared memory that their size needs."""
+    import sys
+    import threading
+    import torch
+    lib = tsd.load_library()
+    sizes, wrong = (440, 512), []
+    inputs = {n: (i32([0, n, 2 * n]), i32(list(range(-1, n - 1)) * 2), i32([0])) for n in sizes}
+    outs = [(i32(np.zeros((2 * sizes[i % 2], 16))), i32(np.zeros(2 * sizes[i % 2])), torch.cuda.Stream()) for i in range(8)]
+    torch.cuda.synchronize()
+
+    def work(i):
+        n = sizes[i % 2]
+        (ip, parents, st), (mask, depth, stream) = inputs[n], outs[i]
+        args = (2, ip.data_ptr(), 2 * n, n, parents.data_ptr(), mask.data_ptr(), depth.data_ptr(), st.data_ptr(),
+                stream.cuda_stream)
+        wrong.extend(x for x in (lib.tsd_tree_mask(*args) for _ in range(4000)) if x)
+
+    interval = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+    try:
+        for t in threads:
+            t.start()
+    finally:
+        for t in threads:
+            t.join()
+        sys.setswitchinterval(interval)
+    torch.cuda.synchronize()
+    assert not wrong, (len(wrong), set(wrong))
+    for i, (_, depth, _) in enumerate(outs):
+        n = sizes[i % 2]
+        assert depth.tolist() == list(range(n)) * 2 and int(inputs[n][2]) == 0

@@ -19,6 +19,7 @@ constexpr int kMaxTree = 512;   // drafts of a sequence
 // ceil(log2 n) rounds over shared memory instead of n dependent steps.  4 to 5 us for 1 to 37 trees with
 // the launch, which is what bounds it.
 constexpr int kTmThreads = 256;
+constexpr size_t tree_mask_smem(int drafts, int words) { return (size_t)2 * drafts * (1 + words) * sizeof(int32_t); }
 
 struct TreeMaskArgs {
   const int32_t* q_indptr;
@@ -1372,9 +1373,10 @@ tsd_status tsd_tree_mask(int32_t batch, const int32_t* q_indptr, int32_t num_tok
   a.num_tokens = num_tokens;
   a.max_tokens = max_tokens;
   a.words = (max_tokens + 31) / 32;
-  const size_t smem = (size_t)2 * max_tokens * (1 + a.words) * sizeof(int32_t);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(tree_mask_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const size_t smem = tree_mask_smem(max_tokens, a.words);
+  if (smem > 48 * 1024) {   // the largest trees' size, whatever this call's: another thread may be about to launch
+    const cudaError_t e = cudaFuncSetAttribute(tree_mask_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)tree_mask_smem(kMaxTree, kMaxTree / 32));
     if (e != cudaSuccess) return TSD_ERR_CUDA;
   }
   tree_mask_kernel<<<batch, kTmThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
