@@ -179,3 +179,27 @@ def test_trees_of_different_sizes_from_several_host_threads():
     for i, (_, depth, _) in enumerate(outs):
         n = sizes[i % 2]
         assert depth.tolist() == list(range(n)) * 2 and int(inputs[n][2]) == 0
+
+
+@pytest.mark.parametrize("shrink,grow", [(128, 128), (700, 700)])
+def test_pages_that_refs_has_as_free_are_not_released_from_their_new_holder(shrink, grow):
+    """Tables name pages that refs has as free, and the call that ends those sequences hands the pages out: whoever comes
+    first, the new holders' counts stand."""
+    import torch
+    B, per = shrink + grow, 4
+    pool = torch.zeros(shrink * per, 1, 2, 128, dtype=torch.bfloat16, device="cuda")
+    for seed in range(20):
+        rng = np.random.default_rng(seed)
+        who = rng.permutation(B)
+        table, lens, new = np.full((B, per), -1), np.zeros(B, int), np.zeros(B, int)
+        table[who[:shrink]] = rng.permutation(shrink * per).reshape(shrink, per)
+        lens[who[:shrink]], new[who[shrink:]] = 2 * per, 2 * per
+        refs, st = i32(np.zeros(shrink * per)), i32([0])
+        cache = tsd.KVCache(pool, pool, i32(lens), 2 * per, page_table=i32(table))
+        tsd.cache_resize(cache, refs, i32(new), status=st)
+        assert int(st) == tsd.DEV_BAD_PAGE
+        assert (refs == 1).all(), int((refs != 1).sum())
+        held = cache.page_table.cpu().numpy()
+        assert (held[who[:shrink]] == -1).all()
+        assert held[np.sort(who[shrink:])].ravel().tolist() == list(range(shrink * per))
+        assert cache.seq_lens.tolist() == new.tolist()

@@ -76,7 +76,9 @@ __global__ void __launch_bounds__(256) cache_fork_kernel(Pool p, int num_pairs, 
 //      counts the free pages of its slice of refs, keeping the first kRzKept groups' as bits;
 //   2  the warps whose first free page has a rank below the total wanted list their free pages;
 //   3  a warp per sequence hands out the listed pages, updates its row and the counts.
-// Sequences are served from the list in order, so the outcome does not depend on timing.  A call
+// Sequences are served from the list in order, so the outcome does not depend on timing.  Where a table names
+// a page that refs has as free, that page may be handed out in the same call; so where a call both
+// releases and takes, all releases (which leave such a page alone) come first, behind one more cluster barrier.  A call
 // is a chain of dependent loads (length, page, count; listed page, row) more than it is bytes: 18 us
 // for 256 sequences over a pool with 70000 free pages, whose bytes take 0.1.
 constexpr int kRzCtas = 8;
@@ -90,7 +92,7 @@ struct ResizeArgs {
   Pool p;
   const int32_t* new_lens;
   int32_t* counts;   // [kRzCounters] free pages of each warp's slice
-  int32_t* total;    // [1] pages wanted in all
+  int32_t* total;    // [2] pages wanted in all, whether any are released
   int2* want;        // [batch] (first rank, pages wanted | copy flag << 31); -1 first: leave alone
   int2* pairs;       // [batch] (from, to) page to copy, (-1, -1) for none
   int32_t* list;     // [num_pages] the free pages of ranks below the total
@@ -139,7 +141,7 @@ __global__ void __cluster_dims__(kRzCtas, 1, 1) __launch_bounds__(kRzThreads) ca
   int64_t g0 = 0, g1 = 0;
   uint32_t kept = 0;
   if (blockIdx.x == 0) {
-    int running = 0;
+    int running = 0, shrinks = 0;
     for (int b0 = 0; b0 < p.batch; b0 += kRzThreads) {
       const int b = b0 + tid;
       int need = 0, cow = 0;
@@ -157,6 +159,8 @@ __global__ void __cluster_dims__(kRzCtas, 1, 1) __launch_bounds__(kRzThreads) ca
             if (page < 0 || (int64_t)page >= p.num_pages) flag_optional(a.status, TSD_DEV_BAD_PAGE);
             else cow = p.refs[page] > 1;
           }
+        } else {
+          shrinks |= now < old;
         }
       }
       int sum;
@@ -164,7 +168,11 @@ __global__ void __cluster_dims__(kRzCtas, 1, 1) __launch_bounds__(kRzThreads) ca
       running += sum;
       if (b < p.batch) a.want[b] = make_int2(ok ? first : -1, (need + cow) | (cow << 31));
     }
-    if (tid == 0) *a.total = running;
+    shrinks = __syncthreads_or(shrinks);
+    if (tid == 0) {
+      a.total[0] = running;
+      a.total[1] = shrinks;
+    }
   } else {
     const int64_t groups = (p.num_pages + 127) / 128;
     g0 = groups * cw / kRzCounters;
@@ -181,7 +189,8 @@ __global__ void __cluster_dims__(kRzCtas, 1, 1) __launch_bounds__(kRzThreads) ca
   }
   cluster_sync();
   // ---- 2
-  const int total = *a.total;
+  const int total = a.total[0];
+  const bool apart = total > 0 && a.total[1];   // releases first
   int2 w = gw < p.batch ? a.want[gw] : make_int2(-1, 0);   // step 3's first sequence
   int old = gw < p.batch ? p.lens[gw] : 0, now = gw < p.batch ? a.new_lens[gw] : 0;
   int before = 0, free_all = 0;
@@ -208,62 +217,67 @@ __global__ void __cluster_dims__(kRzCtas, 1, 1) __launch_bounds__(kRzThreads) ca
   }
   cluster_sync();
   // ---- 3
-  for (int b = gw; b < p.batch; b += kRzWarps) {
-    if (b != gw) {
-      w = a.want[b];
-      old = p.lens[b];
-      now = a.new_lens[b];
-    }
-    int2 pair = make_int2(-1, -1);
-    if (w.x >= 0) {
-      const int need = w.y & 0x7fffffff, cow = (int)((uint32_t)w.y >> 31);
-      const int have = pages_of(old, p.page_shift), end = pages_of(now, p.page_shift);
-      int32_t* row = p.table + (int64_t)b * p.max_pages;
-      if (need > 0 && (int64_t)w.x + need > free_all) {
-        if (lane == 0) flag_optional(a.status, TSD_DEV_NO_PAGES);
-      } else {
-        if (cow) {
-          pair = make_int2(row[have - 1], a.list[w.x]);
-          __syncwarp();
-          if (lane == 0) {
-            row[have - 1] = pair.y;
-            p.refs[pair.y] = 1;
-            atomicSub(p.refs + pair.x, 1);
-          }
-        }
-        for (int i = have + lane; i < end; i += 32) {
-          const int32_t page = a.list[w.x + cow + i - have];
-          row[i] = page;
-          p.refs[page] = 1;
-        }
-        // eight rounds' loads, then their counts, at once: an ended sequence gives back hundreds of pages
-        for (int i0 = end + lane; i0 < have; i0 += 32 * kRzRelease) {
-          int32_t page[kRzRelease], held[kRzRelease];
-#pragma unroll
-          for (int e = 0; e < kRzRelease; ++e) {
-            page[e] = i0 + 32 * e < have ? row[i0 + 32 * e] : 0;
-            held[e] = 1;
-          }
-#pragma unroll
-          for (int e = 0; e < kRzRelease; ++e) {
-            if (i0 + 32 * e >= have) continue;
-            row[i0 + 32 * e] = -1;
-            if (page[e] < 0 || (int64_t)page[e] >= p.num_pages) flag_optional(a.status, TSD_DEV_BAD_PAGE);
-            else held[e] = atomicSub(p.refs + page[e], 1);
-          }
-#pragma unroll
-          for (int e = 0; e < kRzRelease; ++e) {
-            if (held[e] < 1) {   // it was free already
-              atomicAdd(p.refs + page[e], 1);
-              flag_optional(a.status, TSD_DEV_BAD_PAGE);
+#pragma unroll 1
+  for (int pass = apart ? 0 : 1; pass < 2; ++pass) {
+    if (pass == 1 && apart) cluster_sync();
+    for (int b = gw; b < p.batch; b += kRzWarps) {
+      if (b != gw || (apart && pass == 1 && p.batch > kRzWarps)) {   // else they are at hand
+        w = a.want[b];
+        old = p.lens[b];
+        now = a.new_lens[b];
+      }
+      if (apart && (now < old) != (pass == 0)) continue;   // done sequences come by again with their new length
+      int2 pair = make_int2(-1, -1);
+      if (w.x >= 0) {
+        const int need = w.y & 0x7fffffff, cow = (int)((uint32_t)w.y >> 31);
+        const int have = pages_of(old, p.page_shift), end = pages_of(now, p.page_shift);
+        int32_t* row = p.table + (int64_t)b * p.max_pages;
+        if (need > 0 && (int64_t)w.x + need > free_all) {
+          if (lane == 0) flag_optional(a.status, TSD_DEV_NO_PAGES);
+        } else {
+          if (cow) {
+            pair = make_int2(row[have - 1], a.list[w.x]);
+            __syncwarp();
+            if (lane == 0) {
+              row[have - 1] = pair.y;
+              p.refs[pair.y] = 1;
+              atomicSub(p.refs + pair.x, 1);
             }
           }
+          for (int i = have + lane; i < end; i += 32) {
+            const int32_t page = a.list[w.x + cow + i - have];
+            row[i] = page;
+            p.refs[page] = 1;
+          }
+          // eight rounds' loads, then their counts, at once: an ended sequence gives back hundreds of pages
+          for (int i0 = end + lane; i0 < have; i0 += 32 * kRzRelease) {
+            int32_t page[kRzRelease], held[kRzRelease];
+#pragma unroll
+            for (int e = 0; e < kRzRelease; ++e) {
+              page[e] = i0 + 32 * e < have ? row[i0 + 32 * e] : 0;
+              held[e] = 1;
+            }
+#pragma unroll
+            for (int e = 0; e < kRzRelease; ++e) {
+              if (i0 + 32 * e >= have) continue;
+              row[i0 + 32 * e] = -1;
+              if (page[e] < 0 || (int64_t)page[e] >= p.num_pages) flag_optional(a.status, TSD_DEV_BAD_PAGE);
+              else held[e] = atomicSub(p.refs + page[e], 1);
+            }
+#pragma unroll
+            for (int e = 0; e < kRzRelease; ++e) {
+              if (held[e] < 1) {   // it was free already
+                atomicAdd(p.refs + page[e], 1);
+                flag_optional(a.status, TSD_DEV_BAD_PAGE);
+              }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) p.lens[b] = now;
         }
-        __syncwarp();
-        if (lane == 0) p.lens[b] = now;
       }
+      if (lane == 0) a.pairs[b] = pair;
     }
-    if (lane == 0) a.pairs[b] = pair;
   }
 }
 
@@ -473,7 +487,7 @@ static ResizeLayout resize_layout(int64_t batch, int64_t num_pages) {
   ResizeLayout l;
   l.counts = 0;
   l.total_off = kRzCounters * sizeof(int32_t);
-  l.want = align256(l.total_off + sizeof(int32_t));
+  l.want = align256(l.total_off + 2 * sizeof(int32_t));
   l.pairs = l.want + align256((size_t)batch * sizeof(int2));
   l.list = l.pairs + align256((size_t)batch * sizeof(int2));
   l.total = l.list + align256((size_t)num_pages * sizeof(int32_t));
