@@ -203,3 +203,15 @@ def test_pages_that_refs_has_as_free_are_not_released_from_their_new_holder(shri
         assert (held[who[:shrink]] == -1).all()
         assert held[np.sort(who[shrink:])].ravel().tolist() == list(range(shrink * per))
         assert cache.seq_lens.tolist() == new.tolist()
+
+
+def test_counts_do_not_fall_below_zero():
+    """Three sequences hold a page that refs counts twice, and all of them grow out of it."""
+    import torch
+    pool = torch.zeros(8, 1, 4, 128, dtype=torch.bfloat16, device="cuda")
+    table = i32([[3, -1], [3, -1], [3, -1]])
+    refs, st = i32([0, 0, 0, 2, 0, 0, 0, 0]), i32([0])
+    cache = tsd.KVCache(pool, pool, i32([2, 2, 2]), 8, page_table=table)
+    tsd.cache_resize(cache, refs, i32([3, 3, 3]), status=st)
+    assert int(st) == tsd.DEV_BAD_PAGE
+    assert refs.tolist() == [1, 1, 1, 0, 0, 0, 0, 0] and table[:, 0].tolist() == [0, 1, 2]

@@ -241,7 +241,10 @@ __global__ void __cluster_dims__(kRzCtas, 1, 1) __launch_bounds__(kRzThreads) ca
             if (lane == 0) {
               row[have - 1] = pair.y;
               p.refs[pair.y] = 1;
-              atomicSub(p.refs + pair.x, 1);
+              if (atomicSub(p.refs + pair.x, 1) < 1) {   // more tables name it than refs counts
+                atomicAdd(p.refs + pair.x, 1);
+                flag_optional(a.status, TSD_DEV_BAD_PAGE);
+              }
             }
           }
           for (int i = have + lane; i < end; i += 32) {
