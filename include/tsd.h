@@ -507,7 +507,8 @@ tsd_status tsd_rope_init(tsd_rope* rope, int32_t rotary_dim, double theta, int32
  * q_stride, k_stride, v_stride: elements from token to token (heads 128 apart), each a multiple
  *   of 16 bytes and at least heads x 128; slices of one fused projection work.
  * positions, depth: device int32 [T] or NULL, not both.
- * out_q: device, q's type, [T][Hq][128] contiguous; may be q itself when q is contiguous.
+ * out_q: device, q's type, [T][Hq][128] contiguous; may be q itself when q is contiguous, and overlaps none of
+ *   the inputs otherwise.
  * All rows 16-byte aligned.  Errors: INVALID_ARGUMENT, UNSUPPORTED, CUDA.
  */
 tsd_status tsd_rope_append(const tsd_kv_cache* cache, const tsd_queries* queries, const tsd_rope* rope,
@@ -545,7 +546,7 @@ size_t tsd_tree_decode_workspace_size(const tsd_kv_cache* cache, const tsd_queri
  * its output, whatever they hold.
  * mask: device uint32 [T][W], W = ceil(max_tokens_per_seq / 32), or NULL: draft j sees the drafts
  *   up to itself, as tsd_dense_decode with causal set.  queries->causal must be nonzero.
- * out, out_dtype, lse: as tsd_dense_decode.  max_tokens_per_seq <= 512.
+ * out, out_dtype, lse: as tsd_dense_decode; out does not overlap q.  max_tokens_per_seq <= 512.
  * ws: at least tsd_tree_decode_workspace_size bytes, 256-byte aligned, not initialised.
  * Errors: as tsd_dense_decode; UNSUPPORTED for max_tokens_per_seq > 512.
  */

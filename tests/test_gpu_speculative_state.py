@@ -215,3 +215,23 @@ def test_counts_do_not_fall_below_zero():
     tsd.cache_resize(cache, refs, i32([3, 3, 3]), status=st)
     assert int(st) == tsd.DEV_BAD_PAGE
     assert refs.tolist() == [1, 1, 1, 0, 0, 0, 0, 0] and table[:, 0].tolist() == [0, 1, 2]
+
+
+def test_outputs_that_overlap_inputs_are_refused():
+    import torch
+    cache, _ = make_cache([40, 30], 2, 16, fill="other")
+    buf = torch.zeros(2 * 6 * 4 * 128, device="cuda").bfloat16()
+    q, ip = buf[:6 * 512].view(6, 4, 128), i32([0, 3, 6])
+    shifted = buf[512:7 * 512].view(6, 4, 128)
+    x = torch.zeros(6, 2, 128, device="cuda").bfloat16()
+    rope = tsd.RotaryEmbedding()
+    with pytest.raises(tsd.TsdError):
+        tsd.rope_append(cache, rope, q, x, x, ip, 3, out_q=shifted)
+    with pytest.raises(tsd.TsdError):
+        tsd.rope_append(cache, rope, q, buf[6 * 512:9 * 512].view(6, 2, 128), x, ip, 3, out_q=shifted)
+    assert tsd.rope_append(cache, rope, q, x, x, ip, 3, out_q=q) is q
+    assert tsd.rope_append(cache, rope, q, x, x, ip, 3, out_q=buf[6 * 512:].view(6, 4, 128)).shape == q.shape
+    for out in (q, shifted):
+        with pytest.raises(tsd.TsdError):
+            tsd.tree_decode(cache, tsd.Queries(q, ip, 3), out=out)
+    tsd.tree_decode(cache, tsd.Queries(q, ip, 3), out=buf[6 * 512:].view(6, 4, 128))

@@ -6,8 +6,8 @@ import pytest
 import torch
 
 import top_sparse_decode_topk_b200 as tsd
-from tests.test_abi import FAKE, fake_pointer_call, lib, make_cache   # noqa: F401
-from top_sparse_decode_topk_b200 import _LayerC, speculative
+from tests.test_abi import FAKE, fake_pointer_call, lib, make_cache, make_queries   # noqa: F401
+from top_sparse_decode_topk_b200 import _LayerC, _RopeC, speculative
 
 
 def kv(lens, table, pages=5, max_len=16):
@@ -96,3 +96,33 @@ def test_pages_wanted_fit_32_bits(lib):
     assert resize(batch=1, max_pages=2 ** 31 - 2) == small
     assert resize(batch=1, max_pages=2 ** 31 - 1) == tsd.TSD_ERR_UNSUPPORTED
     assert resize(batch=2, max_pages=2 ** 30) == tsd.TSD_ERR_UNSUPPORTED
+
+
+@fake_pointer_call
+def test_outputs_that_overlap_inputs_are_refused(lib):
+    """A row may be rotated onto itself; anything else would be read after it is written."""
+    T, hq, hkv = 64, 32, 8
+    c = make_cache()
+    bytes_q, bytes_k = T * hq * 256, T * hkv * 256
+
+    def append(out, q=FAKE + 0x1000000, q_stride=4096, k=FAKE + 0x2000000, v=FAKE + 0x3000000, tokens=T):
+        qs = make_queries(q=q, tokens=tokens, q_indptr=FAKE, max_tokens=16)
+        r = _RopeC()
+        r.rotary_dim = 128
+        return lib.tsd_rope_append(ctypes.byref(c), ctypes.byref(qs), ctypes.byref(r), q_stride, k, 1024, v, 1024, None, None,
+                                   out, None, None)
+    invalid, q = tsd.TSD_ERR_INVALID_ARGUMENT, FAKE + 0x1000000
+    fine = lambda status: status in (tsd.TSD_OK, tsd.TSD_ERR_CUDA)   # no GPU: the launch itself fails
+    assert append(q + 256) == invalid and append(q - 256) == invalid
+    assert append(q, q_stride=8192) == invalid                       # in place, but rows move
+    assert fine(append(q)) and fine(append(q, q_stride=8192, tokens=1))
+    assert fine(append(q + bytes_q)) and fine(append(q - bytes_q))
+    assert append(FAKE + 0x2000000) == invalid and append(FAKE + 0x3000000 + bytes_k - 16) == invalid
+    assert fine(append(FAKE + 0x2000000 + bytes_k))
+
+    def decode(out, dt):
+        qs = make_queries(q=q, tokens=T, q_indptr=FAKE, max_tokens=16)
+        return lib.tsd_tree_decode(ctypes.byref(c), ctypes.byref(qs), None, out, dt, None, FAKE, 1 << 40, None, None)
+    assert decode(q, 0) == invalid and decode(q + bytes_q - 16, 0) == invalid
+    assert decode(q - bytes_q, 1) == invalid                         # fp32 outputs are twice as long
+    assert fine(decode(q - bytes_q, 0)) and fine(decode(q + bytes_q, 1))

@@ -38,6 +38,12 @@ tsd_status make_kv_maps(const tsd_kv_cache* c, KvMaps* maps, int max_box = 16, b
 // SM count of the current device (148 when none can be queried).
 int current_sm_count();
 
+// Whether two arrays share memory.
+inline bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
 inline tsd_status cuda_status(cudaError_t e) { return e == cudaSuccess ? TSD_OK : TSD_ERR_CUDA; }
 
 }  // namespace tsd

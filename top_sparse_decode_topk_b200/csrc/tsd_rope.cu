@@ -279,6 +279,13 @@ tsd_status tsd_rope_append(const tsd_kv_cache* cache, const tsd_queries* queries
       q_stride % per16 || k_stride % per16 || v_stride % per16)
     return TSD_ERR_INVALID_ARGUMENT;
   if (((uintptr_t)k_new | (uintptr_t)v_new | (uintptr_t)out_q) & 15) return TSD_ERR_INVALID_ARGUMENT;
+  // blocks write out_q while others read: only a row onto itself is safe
+  const int64_t T = sh.tokens, esz = a.qv.q_f32 ? 4 : 2, out_bytes = T * sh.hq * kHeadDim * esz;
+  auto span = [&](int64_t stride, int64_t heads) { return ((T - 1) * stride + heads * kHeadDim) * esz; };
+  const bool in_place = out_q == a.qv.q && (T == 1 || q_stride == sh.hq * kHeadDim);
+  if ((!in_place && overlap(out_q, out_bytes, a.qv.q, span(q_stride, sh.hq))) ||
+      overlap(out_q, out_bytes, k_new, span(k_stride, sh.hkv)) || overlap(out_q, out_bytes, v_new, span(v_stride, sh.hkv)))
+    return TSD_ERR_INVALID_ARGUMENT;
   a.rope = *rope;
   a.rope.interleaved = rope->interleaved != 0;
   a.k_new = k_new;

@@ -1410,6 +1410,10 @@ tsd_status tsd_tree_decode(const tsd_kv_cache* cache, const tsd_queries* queries
   a.ctas = current_sm_count();
   const TreeLayout l = tree_layout(sh, a.ctas, a.qv.q_f32, out_dtype == TSD_F32);
   if (ws_bytes < l.total) return TSD_ERR_WORKSPACE_TOO_SMALL;
+  // outputs are written while other blocks read queries
+  const int64_t elems = sh.tokens * sh.hq * kHeadDim;
+  if (overlap(out, elems * (out_dtype == TSD_F32 ? 4 : 2), a.qv.q, elems * (a.qv.q_f32 ? 4 : 2)))
+    return TSD_ERR_INVALID_ARGUMENT;
   const int64_t groups = (sh.group * sh.max_tokens + 31) / 32;
   // the line of tiles and the merge's grid are counted in 32 bits
   if ((double)sh.batch * sh.hkv * groups * ((double)sh.max_seq_len / 32 + 8) >= 2147483647.0) return TSD_ERR_UNSUPPORTED;
