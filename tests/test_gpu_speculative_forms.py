@@ -6,6 +6,7 @@ import pytest
 import top_sparse_decode_topk_b200 as tsd
 from oracle import speculative as S
 from tests.test_gpu_speculative import compact_case, i32, rope_case, run_tree, status
+from tests.test_gpu_tree_wide import compare, expected, filled
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +64,32 @@ def test_resize_over_more_pages_than_a_warp_keeps(offset):
         assert np.array_equal(lens.cpu().numpy(), model.lens)
         assert status() == sum({"NO_PAGES": tsd.DEV_NO_PAGES}[f] for f in model.flags)
         model.flags.clear()
+
+
+@pytest.mark.parametrize("page", [1, 2, 4, 8, 32, 128])
+@pytest.mark.parametrize("qt,ot", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32")])
+def test_tree_bad_pages_of_every_size(qt, ot, page):
+    """Rows of unreadable pages, among the committed tokens and the drafts, drop out, whatever other pages hold."""
+    import torch
+    n, length, hkv, hq = 20, 700, 2, 8
+    dts = {"bf16": torch.bfloat16, "f32": torch.float32}
+    cache, table = filled([length, length - 300], hkv, page, page, spare=9)
+    used = np.zeros(cache.k.shape[0], bool)
+    used[table[table >= 0]] = True
+    bad = sorted({p // page * page for p in (0, 130, 131, 333, length - 15)})
+    for x in (cache.k, cache.v):
+        x[torch.from_numpy(~used).cuda()] = float("nan")
+        for p in bad:                                          # the pages that are named no more
+            x[int(table[0, p // page])] = float("nan")
+    for i, p in enumerate(bad):
+        cache.page_table[0, p // page] = (-1, 10 ** 9, cache.k.shape[0], -2 ** 31)[i % 4]
+    gone = np.concatenate([np.arange(p, min(length, p + page)) for p in bad])
+    q = torch.randn(n + 3, hq, 128, device="cuda").to(dts[qt])
+    st = i32([0])
+    out, lse = tsd.tree_decode(cache, tsd.Queries(q, i32([0, n, n + 3]), n), None, out_dtype=dts[ot], status=st)
+    assert int(st) == tsd.DEV_BAD_PAGE
+    for row, t0, m, end, lost in ((table[0], 0, n, length, gone), (table[1], n, 3, length - 300, ())):
+        # the formula's copy of a lost row is any number: it is masked
+        k = tsd.KVCache(torch.nan_to_num(cache.k), torch.nan_to_num(cache.v), cache.seq_lens, length, page_table=cache.page_table)
+        compare(out[t0:t0 + m], lse[t0:t0 + m], *expected(k, row, page, q, t0, m, end, np.tril(np.ones((m, m), bool)),
+                                                          1 / np.sqrt(128), lost), ot == "bf16")
