@@ -126,3 +126,11 @@ def test_outputs_that_overlap_inputs_are_refused(lib):
     assert decode(q, 0) == invalid and decode(q + bytes_q - 16, 0) == invalid
     assert decode(q - bytes_q, 1) == invalid                         # fp32 outputs are twice as long
     assert fine(decode(q - bytes_q, 0)) and fine(decode(q + bytes_q, 1))
+
+
+def test_workspace_size_and_call_take_the_same_queries(lib):
+    """Without q_indptr there is one token a sequence, whatever max_tokens_per_seq says."""
+    c = make_cache()
+    size = lambda **kw: lib.tsd_tree_decode_workspace_size(ctypes.byref(c), ctypes.byref(make_queries(**kw)), 0)
+    assert size(max_tokens=600) == size(max_tokens=1) > 0
+    assert size(tokens=2000, q_indptr=FAKE, max_tokens=513) == 0 < size(tokens=2000, q_indptr=FAKE, max_tokens=512)

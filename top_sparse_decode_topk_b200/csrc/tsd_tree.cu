@@ -1385,7 +1385,7 @@ tsd_status tsd_tree_mask(int32_t batch, const int32_t* q_indptr, int32_t num_tok
 
 size_t tsd_tree_decode_workspace_size(const tsd_kv_cache* cache, const tsd_queries* queries, int32_t out_dtype) {
   Shapes sh;
-  if (queries == nullptr || queries->max_tokens_per_seq > kMaxTree) return 0;
+  if (queries == nullptr || (queries->q_indptr != nullptr && queries->max_tokens_per_seq > kMaxTree)) return 0;
   const tsd_queries q = bound_tokens(*queries);
   if (sizes_for(cache, &q, &sh) != TSD_OK) return 0;
   if (out_dtype != TSD_BF16 && out_dtype != TSD_F32) return 0;
