@@ -548,7 +548,8 @@ size_t tsd_tree_decode_workspace_size(const tsd_kv_cache* cache, const tsd_queri
  *   up to itself, as tsd_dense_decode with causal set.  queries->causal must be nonzero.
  * out, out_dtype, lse: as tsd_dense_decode; out does not overlap q.  max_tokens_per_seq <= 512.
  * ws: at least tsd_tree_decode_workspace_size bytes, 256-byte aligned, not initialised.
- * Errors: as tsd_dense_decode; UNSUPPORTED for max_tokens_per_seq > 512.
+ * Errors: as tsd_dense_decode; UNSUPPORTED for max_tokens_per_seq > 512, max_seq_len > 2^31 - 4097, 2^31 or more
+ * rows in K, or lists x tokens that 32 bits cannot number.
  */
 tsd_status tsd_tree_decode(const tsd_kv_cache* cache, const tsd_queries* queries, const uint32_t* mask, void* out,
                            int32_t out_dtype, float* lse, void* ws, size_t ws_bytes, uint32_t* status,

@@ -134,3 +134,14 @@ def test_workspace_size_and_call_take_the_same_queries(lib):
     size = lambda **kw: lib.tsd_tree_decode_workspace_size(ctypes.byref(c), ctypes.byref(make_queries(**kw)), 0)
     assert size(max_tokens=600) == size(max_tokens=1) > 0
     assert size(tokens=2000, q_indptr=FAKE, max_tokens=513) == 0 < size(tokens=2000, q_indptr=FAKE, max_tokens=512)
+
+
+@fake_pointer_call
+def test_positions_behind_a_sequence_fit_32_bits(lib):
+    """A table may name a page many times, so lengths are not bounded by the pool."""
+    def decode(length):
+        c = make_cache(page_size=256, max_pages=2 ** 23, max_seq_len=length, batch=1, hkv=1)
+        q = make_queries(tokens=1, hq=1)
+        return lib.tsd_tree_decode(ctypes.byref(c), ctypes.byref(q), None, FAKE, 0, None, FAKE, 1 << 40, None, None)
+    assert decode(2 ** 31 - 1) == decode(2 ** 31 - 4096) == tsd.TSD_ERR_UNSUPPORTED
+    assert decode(2 ** 31 - 4097) == tsd.TSD_ERR_CUDA   # no GPU: past every check

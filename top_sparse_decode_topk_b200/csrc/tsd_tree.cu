@@ -1415,6 +1415,8 @@ tsd_status tsd_tree_decode(const tsd_kv_cache* cache, const tsd_queries* queries
   if (overlap(out, elems * (out_dtype == TSD_F32 ? 4 : 2), a.qv.q, elems * (a.qv.q_f32 ? 4 : 2)))
     return TSD_ERR_INVALID_ARGUMENT;
   const int64_t groups = (sh.group * sh.max_tokens + 31) / 32;
+  // positions up to a tile (and a producer's 32 boxes) behind a sequence are 32-bit numbers
+  if (sh.max_seq_len > 0x7fffffffLL - 4096) return TSD_ERR_UNSUPPORTED;
   // the line of tiles and the merge's grid are counted in 32 bits
   if ((double)sh.batch * sh.hkv * groups * ((double)sh.max_seq_len / 32 + 8) >= 2147483647.0) return TSD_ERR_UNSUPPORTED;
   a.mask = mask;
