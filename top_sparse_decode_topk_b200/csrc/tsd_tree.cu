@@ -128,8 +128,9 @@ __global__ void __launch_bounds__(kTmThreads) tree_mask_kernel(TreeMaskArgs a) {
 // shared memory (0 x NaN is NaN), and so are drafts' rows that hold infinities or NaNs, whose
 // products are then added for those lists alone that see them.
 //
-// Every wait is bounded; a wait that gives up raises `abort`, after which all waits return at once,
-// the producers issue no more copies, the other loops run out over whatever the buffers hold, and the CTA ends with
+// Every wait is bounded; a wait that gives up raises `abort`, after which all waits return at once.  A
+// producer or an issuer whose wait gave up stops, and no issuer begins another segment, so that a slot of the ring is called empty only when its products are
+// done, and filled only when it is empty; the softmax warps run out over whatever their buffers hold.  The CTA ends with
 // TSD_DEV_TIMEOUT set once its copies and MMAs in flight are through (waited for apart from `abort`).
 struct TreeArgs {
   KvView kv;
@@ -299,16 +300,18 @@ static_assert(sizeof(TreeCtl) <= kTaSmem - kTaTiles, "control block");
 // Bounded wait that gives way to `abort`: up to c->tries tries of up to a microsecond each.  Counted, not
 // timed, to keep the code small: the kernel's waits are many, and an instruction cache miss costs
 // a warp some hundred cycles.
-__device__ __forceinline__ void tree_wait(uint64_t* bar, uint32_t parity, TreeCtl* c, uint32_t* status) {
+// Whether the phase was complete.
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, TreeCtl* c, uint32_t* status) {
 #pragma unroll 1
   for (uint32_t tries = 0; !mbar_try_wait_suspend(bar, parity, 1000u);) {
-    if (*reinterpret_cast<volatile uint32_t*>(&c->abort)) return;
+    if (*reinterpret_cast<volatile uint32_t*>(&c->abort)) return false;
     if (++tries >= c->tries) {
       atomicOr(&c->abort, 1u);
       flag_optional(status, TSD_DEV_TIMEOUT);
-      return;
+      return false;
     }
   }
+  return true;
 }
 // Whether the phase of the given parity is complete.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
@@ -322,14 +325,14 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 
 // tree_wait by all lanes of a warp, converged again behind it (as .aligned instructions need).  Most
 // phases are complete by the time they are waited for, and a test says so sooner than a try.
-__device__ __forceinline__ void tree_wait_warp(uint64_t* bar, uint32_t parity, TreeCtl* c, uint32_t* status) {
-  if (!__all_sync(0xFFFFFFFFu, mbar_test(bar, parity))) {
-    tree_wait(bar, parity, c, status);
-    __syncwarp();
-  }
+// Whether the phase was complete, the same answer for all lanes.
+__device__ __forceinline__ bool tree_wait_warp(uint64_t* bar, uint32_t parity, TreeCtl* c, uint32_t* status) {
+  if (__all_sync(0xFFFFFFFFu, mbar_test(bar, parity))) return true;
+  const bool complete = tree_wait(bar, parity, c, status);
+  return __all_sync(0xFFFFFFFFu, complete);
 }
 
-// Whether a wait of this CTA has given up, the same answer for the whole warp.
+// Whether a wait of this CTA has given up, the same answer for all lanes.
 __device__ __forceinline__ bool tree_gave_up(TreeCtl* c) {
   return __any_sync(0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t*>(&c->abort) != 0);
 }
@@ -1025,12 +1028,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         const int box0 = w * per_tile, boxes = min(per_tile, (len - tile * TT + per - 1) / per);
         if (++w == window) w = 0;
         if ((n & 1) != odd) continue;
-        if (round > 0) {
-          tree_wait_warp(&empty[slot], (round - 1) & 1, ctl, a.status);
-          if (tree_gave_up(ctl)) {   // the slot may still be in use, and its barrier in the phase of its last copies
-            stop = true;
-            break;
-          }
+        if (round > 0 && !tree_wait_warp(&empty[slot], (round - 1) & 1, ctl, a.status)) {
+          stop = true;
+          break;
         }
         if (!is_v) {
           uint32_t* marks = ctl->bad[n & 31];
@@ -1092,31 +1092,37 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       const uint32_t tm = tmem + s * 256;
       uint32_t tiles_done = 0, done = 0, segs = 0;   // segs: those in which this stream has steps
       uint32_t fixes = 0;                            // bit b: parity of the next phase of fixed[s][b]
+      bool stop = false;
 #pragma unroll 1
-      for (; wk.live(); wk.next(a, G)) {
+      for (; wk.live() && !stop; wk.next(a, G)) {
         const bool dual = wk.dual(G);
         const int ntile = wk.k1 - wk.k0, stride = dual ? 1 : 2, first = dual ? 0 : s;
         const int steps = (ntile - first + stride - 1) / stride;
         const uint64_t qd = q_desc + (dual && s ? 32768 >> 4 : 0);
         if (steps > 0) {
-          tree_wait_warp(&ctl->q_ready[s], segs++ & 1, ctl, a.status);
+          // The softmax warps announce queries even when a wait has given up: then the other stream's tiles may not
+          // have come, and a slot's barrier may be a phase behind what a wait here takes it for.
+          if (!tree_wait_warp(&ctl->q_ready[s], segs++ & 1, ctl, a.status) || tree_gave_up(ctl)) break;
           tc_fence_after_sync();
         }
-        auto scores = [&](int i) {
+        auto scores = [&](int i) -> bool {
           const uint32_t n = tiles_done + first + stride * i, slot = n % KS, buf = SH::kSplit ? 0 : (done + i) & 1;
-          tree_wait_warp(&ctl->k_full[slot], (n / KS) & 1, ctl, a.status);
+          if (!tree_wait_warp(&ctl->k_full[slot], (n / KS) & 1, ctl, a.status)) return false;
           tc_fence_after_sync();
-          if (!elect_one()) return;
-          const uint64_t kd = ring_k + (uint64_t)(slot * (SH::kSlotBytes >> 4));
+          if (elect_one()) {
+            const uint64_t kd = ring_k + (uint64_t)(slot * (SH::kSlotBytes >> 4));
 #pragma unroll 1
-          for (int p = QP - 1; p >= 0; --p)   // the small parts first: every step rounds the sum so far
+            for (int p = QP - 1; p >= 0; --p)   // the small parts first: every step rounds the sum so far
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              umma_bf16(tm + buf * 64, qd + ((p * 32768 + (ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
-                        kd + (((ks >> 2) * (TT * 128) + (ks & 3) * 32) >> 4), idesc_s, p < QP - 1 || ks > 0);
-          umma_commit(&ctl->s_full[s][buf]);
-          umma_commit(&ctl->k_empty[slot]);   // expects both streams; a tile of one stream counts twice
-          if (!dual) umma_commit(&ctl->k_empty[slot]);
+              for (int ks = 0; ks < 8; ++ks)
+                umma_bf16(tm + buf * 64, qd + ((p * 32768 + (ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
+                          kd + (((ks >> 2) * (TT * 128) + (ks & 3) * 32) >> 4), idesc_s, p < QP - 1 || ks > 0);
+            umma_commit(&ctl->s_full[s][buf]);
+            umma_commit(&ctl->k_empty[slot]);   // expects both streams; a tile of one stream counts twice
+            if (!dual) umma_commit(&ctl->k_empty[slot]);
+          }
+          __syncwarp();
+          return true;
         };
         // O += P V over the P's tokens, from k step k0 of the tile on; the small parts first
         auto products = [&](uint32_t pt, uint64_t vd, int k0, bool fresh) {
@@ -1133,8 +1139,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             const int at = first + stride * i;
             if (i >= 0) {
               const uint32_t n = tiles_done + at, slot = n % VS, buf = (done + i) & 1;
-              tree_wait_warp(&ctl->v_full[slot], (n / VS) & 1, ctl, a.status);
-              tree_wait_warp(&ctl->p_ready[s][buf], ((done + i) >> 1) & 1, ctl, a.status);
+              stop = !tree_wait_warp(&ctl->v_full[slot], (n / VS) & 1, ctl, a.status) ||
+                     !tree_wait_warp(&ctl->p_ready[s][buf], ((done + i) >> 1) & 1, ctl, a.status);
+              if (stop) break;
               tc_fence_after_sync();
               if (elect_one()) {
                 products(tm + buf * 64, ring_v + (uint64_t)(slot * (SH::kSlotBytes >> 4)), 0,
@@ -1148,30 +1155,33 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             if (i + 2 < steps) {
               if (i >= 0 && (wk.k0 + at + 1) * TT > wk.s.base) {   // a special tile: P is read once more
                 const uint32_t buf = (done + i) & 1;
-                tree_wait_warp(&ctl->fixed[s][buf], fixes >> buf & 1, ctl, a.status);
+                stop = !tree_wait_warp(&ctl->fixed[s][buf], fixes >> buf & 1, ctl, a.status);
+                if (stop) break;
                 fixes ^= 1u << buf;
                 tc_fence_after_sync();
               }
-              scores(i + 2);
-              __syncwarp();
+              stop = !scores(i + 2);
+              if (stop) break;
             }
           }
         } else {
 #pragma unroll 1
           for (int i = -1; i < steps; ++i) {
             if (i + 1 < steps) {   // S(i + 1) is made while the weights of S(i) are
-              if (done + i + 1 > 0) tree_wait_warp(&ctl->s_free[s], (done + i) & 1, ctl, a.status);
+              stop = done + i + 1 > 0 && !tree_wait_warp(&ctl->s_free[s], (done + i) & 1, ctl, a.status);
+              if (stop) break;
               tc_fence_after_sync();
-              scores(i + 1);
-              __syncwarp();
+              stop = !scores(i + 1);
+              if (stop) break;
             }
             if (i < 0) continue;
             const uint32_t n = tiles_done + first + stride * i, slot = n % VS;
             const uint64_t vd = ring_v + (uint64_t)(slot * (SH::kSlotBytes >> 4));
-            tree_wait_warp(&ctl->v_full[slot], (n / VS) & 1, ctl, a.status);
+            stop = !tree_wait_warp(&ctl->v_full[slot], (n / VS) & 1, ctl, a.status);
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-              tree_wait_warp(&ctl->p_ready[s][0], c, ctl, a.status);
+            for (int c = 0; c < 2 && !stop; ++c) {
+              stop = !tree_wait_warp(&ctl->p_ready[s][0], c, ctl, a.status);
+              if (stop) break;
               tc_fence_after_sync();
               if (elect_one()) {
                 products(tm + 64, vd, 2 * c, c == 0 && i % (SH::kFlush ? SH::kFlush : 1) == 0);
@@ -1183,6 +1193,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
               }
               __syncwarp();
             }
+            if (stop) break;
           }
         }
         tiles_done += ntile;
