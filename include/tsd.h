@@ -444,8 +444,11 @@ tsd_status tsd_topk_select_label(const tsd_kv_cache* cache, const void* label_k,
  * status: device uint32 into which TSD_DEV_* bits are OR-ed, or NULL to drop them; the caller
  * clears it (tsd_read_device_status reads and clears it).  These calls keep nothing in their
  * workspace between calls, so it needs no initialisation; two calls that may overlap in time
- * need a workspace each.  Unless stated otherwise, calls may run concurrently when they write
- * different sequences' data.
+ * need a workspace each.  Calls may run concurrently when they write different sequences' data; calls that
+ * write refs (tsd_cache_fork, tsd_cache_resize) may not overlap with one another over one pool, whatever their sequences.
+ *
+ * Drafts that form a tree can be attended to densely only.  Rows that are written, copied or moved here do not reach a
+ * label cache (tsd_label_cache_build) built before: it has to be built again.
  * --------------------------------------------------------------------------------------- */
 
 /* A rotary embedding: pair i < rotary_dim/2 turns by turn[i] per position, in units of 2^-64 of
@@ -467,10 +470,12 @@ typedef enum {
                            f_i / factor for r <= low_freq_factor, f_i for r >= high_freq_factor,
                            linear in r between */
   TSD_ROPE_YARN = 4     /* YaRN (Peng et al., "YaRN: Efficient Context Window Extension of Large
-                           Language Models", 2023, section 3): f_i up to the dim that makes
-                           beta_fast turns over original_max_len (rounded down), f_i / factor from
-                           the dim that makes beta_slow turns (rounded up), linear in i between;
-                           mscale = attention_factor, by default 0.1 ln(factor) + 1 */
+                           Language Models", 2023): f_i up to the dim that makes beta_fast turns
+                           over original_max_len (rounded down), f_i / factor from the dim that
+                           makes beta_slow turns (rounded up), linear in i between, as models of
+                           this kind are configured (the paper's section 3 has a ramp linear in the
+                           number of turns); mscale = attention_factor, by default
+                           0.1 ln(factor) + 1 */
 } tsd_rope_scaling_kind;
 
 typedef struct {
@@ -496,8 +501,8 @@ tsd_status tsd_rope_init(tsd_rope* rope, int32_t rotary_dim, double theta, int32
  *   out_q[t, h]        = R(p) q[t, h]          in q's type
  *   K[row of r, g]     = bf16(R(p) k_new[t, g])
  *   V[row of r, g]     = bf16(v_new[t, g])
- * R(p) turns pair i by p * turn[i]; angles are reduced exactly in 64-bit integers, so they keep
- * fp32 accuracy at any position.  The arithmetic is fp32, rounded once.
+ * R(p) turns pair i by p * turn[i]; angles are reduced exactly in 64-bit integers, so they are good to
+ * 1e-7 radians at any position.  The arithmetic is fp32, rounded once.
  * cache: k and v are written (pages named by the page table; a row whose page id is out of range
  *   is skipped, TSD_DEV_BAD_PAGE).  A page that several sequences hold has to be made private
  *   first (tsd_cache_resize does).
@@ -544,6 +549,9 @@ size_t tsd_tree_decode_workspace_size(const tsd_kv_cache* cache, const tsd_queri
  *   lse[t,h] = M + ln sum over S(t) of exp(z_i - M),   M = max over S(t) of z_i
  * and out = 0, lse = -inf where S(t) is empty.  Rows of V that a draft does not see do not reach
  * its output, whatever they hold.
+ * Scores and softmax statistics are fp32.  With bf16 outputs the weights exp(z_i - M) are rounded to bf16 once before
+ * they multiply V (2^-8 each at most; the sum they are divided by is not rounded): fewer bits than tsd_dense_decode
+ * keeps, and below the outputs' own rounding where several tokens share the weight.  With fp32 outputs they keep 2^-24.
  * mask: device uint32 [T][W], W = ceil(max_tokens_per_seq / 32), or NULL: draft j sees the drafts
  *   up to itself, as tsd_dense_decode with causal set.  queries->causal must be nonzero.
  * out, out_dtype, lse: as tsd_dense_decode; out does not overlap q.  max_tokens_per_seq <= 512.
@@ -590,7 +598,8 @@ size_t tsd_cache_resize_workspace_size(const tsd_kv_cache* cache);
  * first, in order of sequence and position (the replaced last page first).  When the pages wanted
  * by sequences 0 .. b exceed the free ones, a sequence b that wants any is left as it was
  * (TSD_DEV_NO_PAGES).  A new_lens[b] outside [0, max_seq_len] leaves it so too (TSD_DEV_BAD_SEQ).  A
- * table entry out of range is not released (TSD_DEV_BAD_PAGE), nor is a page that refs has as free.
+ * table entry out of range is not released (TSD_DEV_BAD_PAGE), nor is a page that refs has as free: where tables
+ * name a page more often than refs counts, its count stays at 0 (TSD_DEV_BAD_PAGE).
  * cache: paged; its page_table and seq_lens are WRITTEN.  refs: as tsd_cache_fork, written.
  * layers: host array of num_layers (1 .. 128) layers' K and V, each laid out like cache->k; pages
  *   are copied in all of them (cache->k and v only if they are among them).

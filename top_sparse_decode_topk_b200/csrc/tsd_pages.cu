@@ -79,8 +79,9 @@ __global__ void __launch_bounds__(256) cache_fork_kernel(Pool p, int num_pairs, 
 // Sequences are served from the list in order, so the outcome does not depend on timing.  Where a table names
 // a page that refs has as free, that page may be handed out in the same call; so where a call both
 // releases and takes, all releases (which leave such a page alone) come first, behind one more cluster barrier.  A call
-// is a chain of dependent loads (length, page, count; listed page, row) more than it is bytes: 18 us
-// for 256 sequences over a pool with 70000 free pages, whose bytes take 0.1.
+// is a chain of dependent loads (length, page, count; listed page, row) more than it is bytes: for 256
+// sequences over a pool with 70000 free pages, whose bytes take 0.1 us, 8 us where all grow or all shrink by a page or
+// two and 16 where some end with hundreds of pages and others grow (2 of it the barrier between).
 constexpr int kRzCtas = 8;
 constexpr int kRzThreads = 1024;
 constexpr int kRzWarps = kRzCtas * kRzThreads / 32;

@@ -3,9 +3,9 @@
 // Pair i of a row is turned by p f_i radians, p the token's position.  In fp32 the product
 // alone would be off by 2^-24 p f_i -- 0.01 radians at p = 128K -- so positions multiply the
 // frequency in units of 2^-64 turns instead: p * turn[i] in 64-bit integers wraps at whole turns
-// by itself, its top 32 bits are the reduced angle to 2^-33 turns (7e-10 radians), and
-// sincospi of that fp32 fraction is exact to fp32 at any position, with no 64-bit floating
-// point and no range reduction.
+// by itself, and its top 32 bits are the reduced angle to 2^-33 turns (7e-10 radians).  sincospi takes that
+// angle as an fp32 fraction of half a turn, rounded to 2^-25 at most (9e-8 radians, near half a turn): the whole error
+// at any position, with no 64-bit floating point and no range reduction.
 //
 // Bound by HBM: a token moves (Hq + Hkv) x 256 B in and out and Hkv x 512 B of V (bf16).  One
 // block takes one or a few tokens of a sequence: its first threads compute the tokens' sines and cosines
@@ -69,7 +69,7 @@ __device__ __forceinline__ void turn_pair(float& a, float& b, const float2 cs) {
 
 // VEC: the rotated dims split into whole 16-byte chunks on both sides of every pair (half layout:
 // rotary_dim a multiple of 16; interleaved: of 8); otherwise element by element (32768 tokens: 344 us;
-// in the half layout a pair's elements then lie at different places of their chunks).
+// in the half layout a pair's elements then lie at different places of their chunks, and it goes by 2-byte accesses).
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float2 cs[kRopeMaxToks][64];

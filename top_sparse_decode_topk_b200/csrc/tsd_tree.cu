@@ -120,8 +120,9 @@ __global__ void __launch_bounds__(kTmThreads) tree_mask_kernel(TreeMaskArgs a) {
 // Precision: fp32 queries enter as three bf16 parts (QP = 3, exact to 2^-24); with fp32 outputs the
 // weights do too (PP = 3).  With bf16 outputs the weights are rounded to bf16 once (2^-8 at most,
 // averaged over the row), as the outputs are; the sum l is always of the unrounded fp32 weights.
-// The 64-list case above: fp32 queries 227 us (three times the score products), fp32 outputs 297 us,
-// both 357 us: there the tensor cores' floor is some 180 us and the longer softmax chain the rest.
+// The 64-list case above: fp32 queries 221 us (three times the score products), fp32 outputs 283 us,
+// both 354 us.  No unit is busy there (captured at 4 x 8K: tensor pipe 35%, tensor memory 39%, DRAM 24%, issue
+// slots 21%): a stream's chain of dependent steps is longer, and sets the pace.
 //
 // Tiles that reach past the committed tokens ("special": drafts, or the end of the sequence) take a
 // longer path: scores are masked by each list's bits; rows of V behind the sequence are zeroed in
@@ -129,9 +130,10 @@ __global__ void __launch_bounds__(kTmThreads) tree_mask_kernel(TreeMaskArgs a) {
 // products are then added for those lists alone that see them.
 //
 // Every wait is bounded; a wait that gives up raises `abort`, after which all waits return at once.  A
-// producer or an issuer whose wait gave up stops, and no issuer begins another segment, so that a slot of the ring is called empty only when its products are
-// done, and filled only when it is empty; the softmax warps run out over whatever their buffers hold.  The CTA ends with
-// TSD_DEV_TIMEOUT set once its copies and MMAs in flight are through (waited for apart from `abort`).
+// producer or an issuer whose wait gave up stops, and no issuer begins another segment, so that a slot of the
+// ring is called empty only when its products are done, and filled only when it is empty; the softmax warps
+// run out over whatever their buffers hold.  The CTA ends with TSD_DEV_TIMEOUT set once its copies and MMAs in
+// flight are through (waited for apart from `abort`).
 struct TreeArgs {
   KvView kv;
   QView qv;
@@ -181,7 +183,7 @@ struct TreeShape {
   // Steps whose products add up in tensor memory before they are moved to fp32 sums in global
   // memory (fp32 outputs only; 0: never).  The tensor cores truncate each sum: measured, V = 1 came out
   // 6.6e-9 low per accumulation, 2e-5 over 80000 tokens.  Every 512, 256, 128 tokens: errors up to 1.5,
-  // 1.25, 0.85 of a plain fp32 form's; 64 bf16 lists over 8 x 32K in 278, 297, 341 us.
+  // 1.25, 0.85 of a plain fp32 form's; 64 bf16 lists over 8 x 32K in 264, 283, 325 us.
   static constexpr int kFlush = PP == 1 ? 0 : 256 / TT;
 };
 
@@ -662,7 +664,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const uint32_t tm = tmem + lanes + s * 256, to = tm + 128;  // S and P (two buffers), O
     float scale = a.qv.sm_scale * 1.44269504088896340736f;   // base-2 units
     // The tensor cores truncate the sums of a score's products: measured, scores come out 2^-23 low on
-    // average, which the scale makes up for (errors of fp32 outputs fall by a fifth, of lse by a third).
+    // average, which the scale makes up for (errors of fp32 outputs fall by a fifth, of lse by a third).  A score
+    // whose products add up without a rounding comes out 2^-23 of itself high by it: a unit in its last place or two.
     if (PP == 3) scale = fmaf(scale, 0x1p-23f, scale);
     float4* sums = a.sums + ((int64_t)blockIdx.x * 2 + s) * 32 * kTaRowsPerStream + row;   // kFlush: this list's sums
     uint32_t done = 0, tiles_done = 0;
@@ -971,8 +974,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     uint64_t *full = is_v ? ctl->v_full : ctl->k_full, *empty = is_v ? ctl->v_empty : ctl->k_empty;
     const uint32_t slots = is_v ? VS : KS;
     // Pages of 4 or more tokens: boxes of `per` rows, one a lane; smaller pages: four rows a lane.
-    // Measured, 8 x 16 drafts over 32K: pages of 8 178 us in boxes, 280 gathered; of 4 253 and 280; of 1
-    // 282 (a copy instruction for every four rows and half row).
+    // Measured, 8 x 16 drafts over 32K: pages of 8 183 us in boxes, 280 gathered; of 4 256 and 280; of 1
+    // 288 (a copy instruction for every four rows and half row).
     const bool paged = a.kv.page_table != nullptr, gather = paged && a.kv.page_shift < 2;
     const int shift = paged ? a.kv.page_shift : 0, in_page = (1 << shift) - 1;
     const int per = !paged ? TT : (gather ? 4 : min(TT, 1 << shift));

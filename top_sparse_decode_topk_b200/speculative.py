@@ -18,7 +18,9 @@ Outputs and scratch are allocated per call on the call's stream unless the calle
 calls on several streams and several captured graphs share nothing.  Device-detected problems set
 bits in `status` (an int32 tensor), else in the workspace when one is passed, else in a word kept per
 device; ``read_device_status`` reads the latter two.  `stream` defaults to the current stream; tensors
-made on another stream have to be ready on it, as for every call of this package.
+made on another stream have to be ready on it, as for every call of this package.  Two calls at once are fine where
+they write different sequences; cache_fork and cache_resize write `refs`, so of those one at a time over a pool.  Trees
+can be attended to densely only, and a LabelIndex does not follow rows written here: build it again.
 """
 
 from __future__ import annotations
