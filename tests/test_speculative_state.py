@@ -27,6 +27,7 @@ def test_lengths_have_to_be_dense():
     with pytest.raises(ValueError, match="seq_lens"):
         tsd.LayerCaches(kv(state, i32(3, 4)))
     tsd.LayerCaches(kv(state.view(-1)[:3], i32(3, 4)))
+    tsd.LayerCaches(kv(i32(3, 1), i32(3, 4)))
 
 
 def test_tables_have_to_be_dense_with_a_row_for_every_sequence():

@@ -116,7 +116,7 @@ def _check_arrays(cache):
     if k.dim() != 4 or k.shape != v.shape or k.shape[3] != 128 or k.dtype != v.dtype or str(k.dtype) != "torch.bfloat16" or \
             not k.is_contiguous() or not v.is_contiguous() or v.device != k.device or lens.device != k.device:
         raise ValueError("k and v must be contiguous bfloat16 tensors of one 4-d shape with head_dim 128, on one device")
-    if lens.dim() != 1 or not lens.is_contiguous():
+    if lens.dim() < 1 or lens.numel() != lens.shape[0] or not lens.is_contiguous():
         raise ValueError("seq_lens must be a contiguous int32 [batch] tensor")
     if table is None:
         if cache.k.shape[0] < lens.shape[0]:
