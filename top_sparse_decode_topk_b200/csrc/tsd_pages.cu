@@ -102,6 +102,7 @@ struct ResizeArgs {
 };
 
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();   // lanes may come from different ends of a loop, and the barrier takes whole warps
   asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }

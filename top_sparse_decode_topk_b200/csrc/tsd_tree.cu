@@ -359,6 +359,7 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
   __syncwarp();
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }
+// Of a whole warp, converged (bar.sync and bar.arrive are aligned instructions).
 __device__ __forceinline__ void pair_wait(int id) { asm volatile("bar.sync %0, 64;\n" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void pair_arrive(int id) { asm volatile("bar.arrive %0, 64;\n" ::"r"(id) : "memory"); }
 __device__ __forceinline__ float max3(float x, float y, float z) {
@@ -681,6 +682,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       const bool valid = list < lists, warp_live = first + 32 * (warp & 3) < lists;
       // the warp of the other stream on the same quarter of the SM has work too
       const bool pair = PP == 1 && dual && wk.mt * SH::kRows + kTaRowsPerStream + 32 * (warp & 3) < lists;
+      __syncwarp();   // lanes without a list left the last segment's stores early
       if (pair && s == 1) pair_arrive(4 + 2 * (warp & 3));   // stream 0 goes first
       const int j = list / G, h = wk.g * G + (list - j * G);
       named_sync(1, 256);   // the previous segment's Q tiles and states are done with
@@ -878,6 +880,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           if (warp_live) l += l2[0].x + l2[0].y;
         }
       }
+      __syncwarp();
       if (pair && s == 0) pair_wait(4 + 2 * (warp & 3));   // the other stream's last turn
       if (steps > 0) products_done(done + steps - 1);
       tc_fence_after_sync();
